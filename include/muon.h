@@ -144,6 +144,31 @@ MUON_API size_t muon_workspace_min(const muon_group* groups, int n_groups, const
 MUON_API int muon_step(const muon_group* groups, int n_groups, const muon_hparams* hp, void* ws, size_t ws_bytes,
               int* status_per_matrix, void* stream);
 
+/* One group of `count` blocks that share a shape rows x cols, each a part of a
+ * larger row-major matrix: a head's rows of an attention projection, its
+ * columns of the output projection, gate or up of a fused weight, an expert of
+ * a stack.  As muon_group, with the row pitch (in elements, at least cols) of
+ * the matrices that the blocks lie in, and pointers that need no more than
+ * their elements' alignment (rows that all start on 16 bytes are moved by
+ * 16-byte accesses, others element by element).  Nothing outside the blocks is
+ * read or written; blocks of one call must not overlap. */
+typedef struct {
+  int rows, cols, count;
+  int w_dtype, g_dtype;
+  long long ld_w, ld_g, ld_m;
+  void* const* W;
+  const void* const* G;
+  float* const* M;
+} muon_block_group;
+
+/* muon_step with every block as a matrix of its own: its own norm, its own
+ * orthogonalisation, and the update scale sqrt(max(rows, cols)) of the block.
+ * A block that is a whole dense matrix gets muon_step's result, bit for bit. */
+MUON_API size_t muon_blocks_workspace_size(const muon_block_group* groups, int n_groups, const muon_hparams* hp);
+MUON_API size_t muon_blocks_workspace_min(const muon_block_group* groups, int n_groups, const muon_hparams* hp);
+MUON_API int muon_step_blocks(const muon_block_group* groups, int n_groups, const muon_hparams* hp, void* ws,
+                              size_t ws_bytes, int* status_per_block, void* stream);
+
 /* In-place orthogonalisation of `count` matrices of storage shape rows x cols
  * and dtype `dtype` (X[i] is a device pointer; O replaces X in the same
  * orientation).  This is the listing's newton_schulz_orthogonalize without
@@ -178,6 +203,75 @@ MUON_API int muon_ns_batched(void* const* X, int count, int rows, int cols, int 
 #define MUON_NOALLOC_SCRATCH_BYTES (64u << 20)
 MUON_API int muon_ns_batched_noalloc(void* const* X, int count, int rows, int cols, int dtype,
                                      const muon_ns_params* ns, int* status_per_matrix, void* stream);
+
+/* ---------------------------------------------------------------- expert layers
+ * What produces the gradients of a mixture-of-experts layer's weights: tokens
+ * sorted by expert and back, and the experts' products with their gradients.
+ *
+ * A router sends each of `tokens` tokens to `topk` of `experts` experts.  An
+ * assignment is a pair (t, j); its number is t * topk + j.
+ *   offsets  device int array, experts + 1: expert e owns the sorted rows
+ *            [offsets[e], offsets[e+1])
+ *   slot     device int array, tokens x topk: the sorted row of an assignment,
+ *            or a negative number for an assignment that no expert takes
+ *   source   device int array, tokens x topk: the assignment behind every sorted
+ *            row; behind the last row, those that no expert takes, in order
+ * Matrices are row-major with a row pitch ld >= cols in elements and any
+ * alignment of their elements; rows that start on 16 bytes are moved faster,
+ * and the 16-bit products need it for the tensor cores (base, pitch and expert
+ * stride multiples of 16 bytes; others run on the CUDA cores).  Sorted rows that
+ * no expert owns are neither read into a result nor written.  All sums are held
+ * in fp32 and rounded once, in an order that does not change from call to call.
+ * Row counts and tokens * topk are at most 2^31 - 1, experts at most 1024.
+ *
+ * muon_expert_sort: ids is tokens x topk of int32 or int64 (id_bytes 4 or 8),
+ * row pitch ld_ids; an id outside [0, experts) goes to no expert.  The sort is
+ * stable: an expert's rows keep the order of their assignments. */
+MUON_API size_t muon_expert_sort_workspace_size(int tokens, int topk, int experts);
+MUON_API int muon_expert_sort(const void* ids, int id_bytes, long long ld_ids, int tokens, int topk, int experts,
+                              int* offsets, int* slot, int* source, void* ws, size_t ws_bytes, void* stream);
+
+/* xs[slot[t, j]] = x[t].  x is tokens x cols, xs is rows x cols; slots of one
+ * call are distinct, and those outside [0, rows) are skipped (here and below).
+ * Its gradient is muon_expert_combine without weights. */
+MUON_API int muon_expert_gather(const void* x, long long ld_x, const int* slot, int tokens, int topk, int cols, int dtype,
+                                void* xs, long long ld_xs, long long rows, void* stream);
+
+/* y[t] = sum_j weights[t, j] * ys[slot[t, j]], j ascending; zero for a token
+ * that no expert takes.  weights is tokens x topk of w_dtype, dense; NULL: ones. */
+MUON_API int muon_expert_combine(const void* ys, long long ld_ys, long long rows, const int* slot, const void* weights,
+                                 int w_dtype, int tokens, int topk, int cols, int dtype, void* y, long long ld_y,
+                                 void* stream);
+
+/* The gradients of muon_expert_combine:
+ *   dys[slot[t, j]]  = weights[t, j] * dy[t]
+ *   dweights[t, j]   = <dy[t], ys[slot[t, j]]>, zero for an assignment that no expert takes
+ * dweights (of w_dtype) may be NULL; ys is then not read. */
+MUON_API int muon_expert_combine_backward(const void* dy, long long ld_dy, const void* ys, long long ld_ys, long long rows,
+                                          const int* slot, const void* weights, int w_dtype, int tokens, int topk,
+                                          int cols, int dtype, void* dys, long long ld_dys, void* dweights, void* stream);
+
+/* The experts' products.  W[e] is outer x inner at w + e * stride_w, row pitch
+ * ld_w; xs is rows x inner, ys and dys are rows x outer, one dtype for all.
+ * Offsets are clamped to [0, rows] and read on the device: no count reaches the
+ * host.
+ *   muon_expert_product       y[p]   = W[e] xs[p]            for e's rows p
+ *   muon_expert_input_grad    dxs[p] = W[e]^T dys[p]         for e's rows p
+ *   muon_expert_weight_grad   dW[e]  = sum_p dys[p] xs[p]^T  over e's rows p
+ * dW[e] (outer x inner at dw + e * stride_dw) has the operands' type or fp32; an
+ * expert without rows gets zeros.  accumulate (fp32 dW only) adds to dW instead.
+ * status: one optional device word, zeroed by the call, MUON_STATUS_TIMEOUT when
+ * a device-side wait gave up. */
+MUON_API int muon_expert_product(const void* xs, long long ld_xs, const void* w, long long ld_w, long long stride_w,
+                                 const int* offsets, int experts, long long rows, int inner, int outer, int dtype,
+                                 void* y, long long ld_y, int* status, void* stream);
+MUON_API int muon_expert_input_grad(const void* dys, long long ld_dys, const void* w, long long ld_w, long long stride_w,
+                                    const int* offsets, int experts, long long rows, int inner, int outer, int dtype,
+                                    void* dxs, long long ld_dxs, int* status, void* stream);
+MUON_API int muon_expert_weight_grad(const void* dys, long long ld_dys, const void* xs, long long ld_xs,
+                                     const int* offsets, int experts, long long rows, int inner, int outer, int dtype,
+                                     void* dw, long long ld_dw, long long stride_dw, int dw_dtype, int accumulate,
+                                     int* status, void* stream);
 
 /* Algorithmic FLOPs of one orthogonalisation of a rows x cols matrix, every
  * product counted as 2 * rows * cols * inner [GramNS cost list]. */

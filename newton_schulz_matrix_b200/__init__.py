@@ -1,5 +1,7 @@
-"""Python binding of libmuon (include/muon.h): the Muon optimizer step and
-batched Newton-Schulz orthogonalisation on NVIDIA B200.
+"""Python binding of libmuon (include/muon.h): the Muon optimizer step (on
+whole matrices, or on the blocks of stacked and fused weights), batched
+Newton-Schulz orthogonalisation, and the expert-layer operators whose weight
+gradients the step takes, on NVIDIA B200.
 
 This module only marshals arguments: it turns torch tensors into device
 pointers, groups, hyper-parameter structs and the current CUDA stream, and calls
@@ -22,7 +24,10 @@ __all__ = [
     "MuonError", "load_library", "library_path", "muon_step", "muon_ns_batched",
     "muon_workspace_size", "muon_workspace_min", "muon_ns_workspace_size", "muon_ns_flops",
     "muon_status_string", "muon_profile_begin", "muon_profile_end", "MuonStep", "StreamedMuonStep",
-    "plan_slices", "muon_ns_batched_noalloc",
+    "plan_slices", "muon_ns_batched_noalloc", "muon_step_blocks", "muon_blocks_workspace_size",
+    "muon_blocks_workspace_min", "muon_expert_sort", "muon_expert_gather", "muon_expert_gather_backward",
+    "muon_expert_combine", "muon_expert_combine_backward", "muon_expert_product", "muon_expert_input_grad",
+    "muon_expert_weight_grad", "ExpertMuonStep", "EXPERT_MAX",
     "NOALLOC_SCRATCH_BYTES", "EXPORTED_SYMBOLS",
 ]
 
@@ -35,8 +40,11 @@ CUBIC = (1.5, -0.5, 0.0)
 EXPORTED_SYMBOLS = (
     "muon_workspace_size", "muon_workspace_min", "muon_step", "muon_ns_workspace_size",
     "muon_ns_batched", "muon_ns_flops", "muon_status_string", "muon_profile_begin", "muon_profile_end",
-    "muon_ns_batched_noalloc",
+    "muon_ns_batched_noalloc", "muon_blocks_workspace_size", "muon_blocks_workspace_min", "muon_step_blocks",
+    "muon_expert_sort_workspace_size", "muon_expert_sort", "muon_expert_gather", "muon_expert_combine",
+    "muon_expert_combine_backward", "muon_expert_product", "muon_expert_input_grad", "muon_expert_weight_grad",
 )
+EXPERT_MAX = 1024
 NOALLOC_SCRATCH_BYTES = 64 << 20
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -56,6 +64,14 @@ class _NSParams(ctypes.Structure):
 class _Group(ctypes.Structure):
     _fields_ = [("rows", ctypes.c_int), ("cols", ctypes.c_int), ("count", ctypes.c_int),
                 ("w_dtype", ctypes.c_int), ("g_dtype", ctypes.c_int),
+                ("W", ctypes.POINTER(ctypes.c_void_p)), ("G", ctypes.POINTER(ctypes.c_void_p)),
+                ("M", ctypes.POINTER(ctypes.c_void_p))]
+
+
+class _BlockGroup(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int), ("cols", ctypes.c_int), ("count", ctypes.c_int),
+                ("w_dtype", ctypes.c_int), ("g_dtype", ctypes.c_int),
+                ("ld_w", ctypes.c_longlong), ("ld_g", ctypes.c_longlong), ("ld_m", ctypes.c_longlong),
                 ("W", ctypes.POINTER(ctypes.c_void_p)), ("G", ctypes.POINTER(ctypes.c_void_p)),
                 ("M", ctypes.POINTER(ctypes.c_void_p))]
 
@@ -101,6 +117,25 @@ def load_library() -> ctypes.CDLL:
     lib.muon_ns_batched_noalloc.argtypes = [ctypes.POINTER(ctypes.c_void_p), ctypes.c_int, ctypes.c_int,
                                             ctypes.c_int, ctypes.c_int, ctypes.POINTER(_NSParams), P, P]
     lib.muon_ns_batched_noalloc.restype = ctypes.c_int
+    for name in ("muon_blocks_workspace_size", "muon_blocks_workspace_min"):
+        getattr(lib, name).argtypes = [ctypes.POINTER(_BlockGroup), ctypes.c_int, ctypes.POINTER(_HParams)]
+        getattr(lib, name).restype = ctypes.c_size_t
+    lib.muon_step_blocks.argtypes = [ctypes.POINTER(_BlockGroup), ctypes.c_int, ctypes.POINTER(_HParams), P,
+                                     ctypes.c_size_t, P, P]
+    I, L = ctypes.c_int, ctypes.c_longlong
+    lib.muon_expert_sort_workspace_size.argtypes = [I, I, I]
+    lib.muon_expert_sort_workspace_size.restype = ctypes.c_size_t
+    lib.muon_expert_sort.argtypes = [P, I, L, I, I, I, P, P, P, P, ctypes.c_size_t, P]
+    lib.muon_expert_gather.argtypes = [P, L, P, I, I, I, I, P, L, L, P]
+    lib.muon_expert_combine.argtypes = [P, L, L, P, P, I, I, I, I, I, P, L, P]
+    lib.muon_expert_combine_backward.argtypes = [P, L, P, L, L, P, P, I, I, I, I, I, P, L, P, P]
+    lib.muon_expert_product.argtypes = [P, L, P, L, L, P, I, L, I, I, I, P, L, P, P]
+    lib.muon_expert_input_grad.argtypes = [P, L, P, L, L, P, I, L, I, I, I, P, L, P, P]
+    lib.muon_expert_weight_grad.argtypes = [P, L, P, L, P, I, L, I, I, I, P, L, L, I, I, P, P]
+    for name in ("muon_step_blocks", "muon_expert_sort", "muon_expert_gather", "muon_expert_combine",
+                 "muon_expert_combine_backward", "muon_expert_product", "muon_expert_input_grad",
+                 "muon_expert_weight_grad"):
+        getattr(lib, name).restype = ctypes.c_int
     lib.muon_profile_begin.argtypes = []
     lib.muon_profile_begin.restype = ctypes.c_int
     lib.muon_profile_end.argtypes = [ctypes.POINTER(_ProfEntry), ctypes.c_int]
@@ -141,6 +176,23 @@ def _stream_handle(stream) -> int:
     if stream is None:
         stream = torch.cuda.current_stream()
     return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _on(device: torch.device, stream, call):
+    """call(stream handle) with ``device`` current and, if a stream is given, that
+    stream current too, so that what the call allocates belongs to it."""
+    if stream is None and device.index == torch.cuda.current_device():
+        return call(torch.cuda.current_stream(device).cuda_stream)
+    with torch.cuda.device(device):
+        if stream is None:
+            return call(torch.cuda.current_stream(device).cuda_stream)
+        if not hasattr(stream, "cuda_stream"):
+            handle = int(stream)
+            stream = torch.cuda.ExternalStream(handle, device=device) if handle else torch.cuda.default_stream(device)
+        if stream.device != device:
+            raise MuonError(f"the stream is on {stream.device}, the tensors on {device}")
+        with torch.cuda.stream(stream):
+            return call(stream.cuda_stream)
 
 
 def _check_cuda(t: torch.Tensor, name: str):
@@ -186,6 +238,71 @@ def _build_groups(params, grads, moms):
     return groups, len(keys), keep, order
 
 
+def _matrices(t: torch.Tensor, es: int):
+    """Addresses of the matrices of (..., R, C), in order."""
+    at = [t.data_ptr()]
+    for n, stride in zip(t.shape[:-2], t.stride()[:-2]):
+        at = [p + i * stride * es for p in at for i in range(n)]
+    return at
+
+
+def _pitch(t: torch.Tensor, name: str) -> int:
+    """The row pitch (in elements) of a matrix, or of the matrices of (..., R, C)."""
+    rows, cols = t.shape[-2:]
+    if cols > 1 and t.stride(-1) != 1:
+        raise MuonError(f"{name} must have contiguous rows")
+    ld = t.stride(-2) if rows > 1 else cols
+    if ld < cols:
+        raise MuonError(f"{name} has overlapping rows")
+    return ld
+
+
+def _build_block_groups(params, grads, moms, blocks):
+    """Block groups in first-appearance order, and the index of every grouped
+    block in the order of the parameters' blocks (matrices, block rows, block
+    columns)."""
+    if len(blocks) != len(params):
+        raise MuonError("blocks must have one entry per parameter")
+    keys, index, total = [], {}, 0
+    for w, g, m, block in zip(params, grads, moms, blocks):
+        for t, name in ((w, "param"), (g, "grad"), (m, "momentum")):
+            if not t.is_cuda:
+                raise MuonError(f"{name} must be a CUDA tensor")
+            if t.dim() < 2 or t.numel() == 0:
+                raise MuonError(f"{name} must have at least two dimensions and no empty one")
+        if w.shape != g.shape or w.shape != m.shape:
+            raise MuonError("param, grad and momentum shapes differ")
+        if m.dtype != torch.float32:
+            raise MuonError("momentum buffers must be float32")
+        rows, cols = w.shape[-2:]
+        r, c = (rows, cols) if block is None else (int(block[0]), int(block[1]))
+        if r < 1 or c < 1 or rows % r or cols % c:
+            raise MuonError(f"blocks of {r} x {c} do not tile a {rows} x {cols} matrix")
+        k = (r, c, _dtype_code(w.dtype), _dtype_code(g.dtype)) + tuple(
+            _pitch(t, n) for t, n in ((w, "param"), (g, "grad"), (m, "momentum")))
+        if k not in index:
+            index[k] = len(keys)
+            keys.append((k, [], [], [], []))
+        entry = keys[index[k]]
+        n = 0
+        for t, ld, out in zip((w, g, m), k[4:], entry[1:4]):
+            es = t.element_size()
+            inside = [(i * ld + j) * es for i in range(0, rows, r) for j in range(0, cols, c)]
+            at = [p + o for p in _matrices(t, es) for o in inside]
+            out.extend(at)
+            n = len(at)
+        entry[4].extend(range(total, total + n))
+        total += n
+    groups = (_BlockGroup * len(keys))()
+    keep, order = [], []
+    for gi, (k, *ptrs, idx) in enumerate(keys):
+        arrays = [(ctypes.c_void_p * len(p))(*p) for p in ptrs]
+        keep += arrays
+        groups[gi] = _BlockGroup(k[0], k[1], len(idx), k[2], k[3], *k[4:], *arrays)
+        order += idx
+    return groups, len(keys), keep, order
+
+
 def _hparams(lr, momentum, weight_decay, scale_coef, nesterov, ns):
     return _HParams(float(lr), float(momentum), float(weight_decay), float(scale_coef), int(bool(nesterov)), ns)
 
@@ -204,10 +321,13 @@ def muon_ns_flops(rows: int, cols: int, coeffs=(QUINTIC,) * 5, mode="standard", 
 
 
 def _step_args(params, grads, moms, lr, momentum, nesterov, weight_decay, scale_coef, eps, coeffs, mode,
-               restart_after, compute_dtype, gram_dtype, restart_every=0):
+               restart_after, compute_dtype, gram_dtype, restart_every=0, blocks=None):
     if not (len(params) == len(grads) == len(moms)) or len(params) == 0:
         raise MuonError("params, grads and moms must be non-empty lists of equal length")
-    groups, ng, keep, order = _build_groups(params, grads, moms)
+    if blocks is None:
+        groups, ng, keep, order = _build_groups(params, grads, moms)
+    else:
+        groups, ng, keep, order = _build_block_groups(params, grads, moms, blocks)
     ns, arr = _ns_params(coeffs, mode, restart_after, eps, compute_dtype, gram_dtype, restart_every)
     hp = _hparams(lr, momentum, weight_decay, scale_coef, nesterov, ns)
     return groups, ng, hp, (keep, arr), order
@@ -268,6 +388,52 @@ def muon_step(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor], mom
     return status
 
 
+def muon_blocks_workspace_size(params, grads, moms, blocks, **hp) -> int:
+    groups, ng, h, _keep, _ = _step_args(params, grads, moms, blocks=blocks, **dict(_STEP_DEFAULTS, **hp))
+    return int(load_library().muon_blocks_workspace_size(groups, ng, ctypes.byref(h)))
+
+
+def muon_blocks_workspace_min(params, grads, moms, blocks, **hp) -> int:
+    groups, ng, h, _keep, _ = _step_args(params, grads, moms, blocks=blocks, **dict(_STEP_DEFAULTS, **hp))
+    return int(load_library().muon_blocks_workspace_min(groups, ng, ctypes.byref(h)))
+
+
+def muon_step_blocks(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor], moms: Sequence[torch.Tensor],
+                     blocks: Sequence, *, workspace: torch.Tensor | None = None, status: torch.Tensor | None = None,
+                     stream=None, **hp) -> torch.Tensor | None:
+    """One Muon step on the blocks of stacked, fused or strided weights, in
+    place on ``params`` and ``moms``.
+
+    A parameter is (..., R, C) with contiguous rows and any other strides (an
+    expert stack, a fused gate and up, a slice of either); its entry in
+    ``blocks`` is the (rows, cols) of the blocks that tile each of its
+    matrices, or None for whole matrices.  Every block is orthogonalised on its
+    own, as muon_step does a matrix: (head_dim, hidden) splits a query
+    projection into heads, (hidden, head_dim) an output projection.  ``status``
+    has one word per block, in the order of the parameters, their matrices,
+    block rows and block columns.  Hyper-parameters as for muon_step.
+    """
+    lib = load_library()
+    groups, ng, h, _keep, order = _step_args(params, grads, moms, blocks=blocks, **dict(_STEP_DEFAULTS, **hp))
+    need = int(lib.muon_blocks_workspace_size(groups, ng, ctypes.byref(h)))
+    if need == 0:
+        raise MuonError("invalid arguments (workspace query returned 0)")
+    device = params[0].device
+    if status is not None and (status.dtype != torch.int32 or status.numel() != len(order) or status.device != device):
+        raise MuonError(f"status must be an int32 tensor of {len(order)} words on the parameters' device")
+
+    def call(handle):
+        ws = torch.empty(need, dtype=torch.uint8, device=device) if workspace is None else workspace
+        grouped = None if status is None else torch.empty(len(order), dtype=torch.int32, device=device)
+        _raise(lib.muon_step_blocks(groups, ng, ctypes.byref(h), ws.data_ptr(), ws.numel() * ws.element_size(),
+                                    None if grouped is None else grouped.data_ptr(), handle), "muon_step_blocks")
+        if status is not None:
+            status.view(-1)[torch.tensor(order, device=device)] = grouped
+        return status
+
+    return _on(device, stream, call)
+
+
 def muon_ns_workspace_size(count: int, rows: int, cols: int, coeffs=(QUINTIC,) * 5, mode="standard",
                            restart_after=2, eps=1e-7, compute_dtype="fp16", gram_dtype="fp16",
                            restart_every=0) -> int:
@@ -323,8 +489,8 @@ def muon_profile_end() -> list[dict]:
     """Stop profiling; per kernel kind: launches, device ms, algorithmic FLOPs,
     executed FLOPs (whole tensor-core tiles, triangles only for symmetric
     products, three MMAs per 3xTF32 product) and algorithmic bytes."""
-    rows = (_ProfEntry * 16)()
-    n = load_library().muon_profile_end(rows, 16)
+    rows = (_ProfEntry * 32)()
+    n = load_library().muon_profile_end(rows, 32)
     if n < 0:
         _raise(n, "muon_profile_end")
     return [dict(kernel=r.kernel.decode(), launches=r.launches, ms=r.ms, flops=r.flops, exec_flops=r.exec_flops,
@@ -336,17 +502,21 @@ class MuonStep:
 
     Builds the C structs (groups, hyper-parameters) and the workspace once, so
     each call is a single C-ABI call with no per-step marshalling.  The tensors
-    must stay alive and keep their storage for the object's lifetime.
+    must stay alive and keep their storage for the object's lifetime.  With
+    ``blocks`` it is muon_step_blocks: one status word per block.
     """
 
     def __init__(self, params, grads, moms, *, workspace_bytes: int | None = None,
-                 workspace: torch.Tensor | None = None, **hp):
+                 workspace: torch.Tensor | None = None, blocks: Sequence | None = None, **hp):
         self._lib = load_library()
         a = dict(_STEP_DEFAULTS, **hp)
         self.hp = a
-        self._groups, self._ng, self._h, self._keep, self.order = _step_args(params, grads, moms, **a)
-        full = int(self._lib.muon_workspace_size(self._groups, self._ng, ctypes.byref(self._h)))
-        lo = int(self._lib.muon_workspace_min(self._groups, self._ng, ctypes.byref(self._h)))
+        self._groups, self._ng, self._h, self._keep, self.order = _step_args(params, grads, moms, blocks=blocks, **a)
+        kind = "muon" if blocks is None else "muon_blocks"
+        self._name = "muon_step" if blocks is None else "muon_step_blocks"
+        self._step = getattr(self._lib, self._name)
+        full = int(getattr(self._lib, kind + "_workspace_size")(self._groups, self._ng, ctypes.byref(self._h)))
+        lo = int(getattr(self._lib, kind + "_workspace_min")(self._groups, self._ng, ctypes.byref(self._h)))
         if full == 0:
             raise MuonError("invalid arguments (workspace query returned 0)")
         self.workspace_needed = (lo, full)
@@ -361,10 +531,10 @@ class MuonStep:
         self.count = len(self.order)
 
     def __call__(self, stream=None) -> None:
-        rc = self._lib.muon_step(self._groups, self._ng, ctypes.byref(self._h),
-                                 ctypes.c_void_p(self.workspace.data_ptr()), ctypes.c_size_t(self.workspace.numel()),
-                                 ctypes.c_void_p(self.status.data_ptr()), ctypes.c_void_p(_stream_handle(stream)))
-        _raise(rc, "muon_step")
+        rc = self._step(self._groups, self._ng, ctypes.byref(self._h), ctypes.c_void_p(self.workspace.data_ptr()),
+                        ctypes.c_size_t(self.workspace.numel()), ctypes.c_void_p(self.status.data_ptr()),
+                        ctypes.c_void_p(_stream_handle(stream)))
+        _raise(rc, self._name)
 
     def capture(self, stream=None) -> "torch.cuda.CUDAGraph":
         """Record one step into a CUDA graph and return it; ``graph.replay()``
@@ -515,3 +685,341 @@ class StreamedMuonStep:
     @property
     def status(self) -> torch.Tensor:
         return torch.cat([st.status_in_param_order() for st in self.steps])
+
+
+# ---------------------------------------------------------------------------
+# expert layers
+# ---------------------------------------------------------------------------
+def _rows_arg(t: torch.Tensor, name: str, device=None, dtype=None, shape=None) -> int:
+    """Checks a 2-D matrix with contiguous rows; returns its row pitch."""
+    if not t.is_cuda:
+        raise MuonError(f"{name} must be a CUDA tensor")
+    if device is not None and t.device != device:
+        raise MuonError(f"{name} is on {t.device}, not on {device}")
+    if t.dim() != 2:
+        raise MuonError(f"{name} must be 2-D")
+    if dtype is not None and t.dtype != dtype:
+        raise MuonError(f"{name} must be {dtype}, not {t.dtype}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise MuonError(f"{name} must be {tuple(shape)}, not {tuple(t.shape)}")
+    return _pitch(t, name)
+
+
+def _slot_arg(slot: torch.Tensor, device=None):
+    if not slot.is_cuda or slot.dtype != torch.int32 or slot.dim() != 2 or not slot.is_contiguous():
+        raise MuonError("slot must be a contiguous 2-D int32 CUDA tensor")
+    if device is not None and slot.device != device:
+        raise MuonError(f"slot is on {slot.device}, not on {device}")
+    if slot.shape[1] < 1:
+        raise MuonError("slot must have at least one column")
+    return slot.shape
+
+
+def _weights_arg(weights: torch.Tensor, slot: torch.Tensor) -> int:
+    if not weights.is_cuda or weights.device != slot.device or not weights.is_contiguous():
+        raise MuonError("weights must be contiguous and on the slots' device")
+    if weights.shape != slot.shape:
+        raise MuonError(f"weights must be {tuple(slot.shape)}, not {tuple(weights.shape)}")
+    return _dtype_code(weights.dtype)
+
+
+def muon_expert_sort(ids: torch.Tensor, experts: int, *, workspace: torch.Tensor | None = None, stream=None):
+    """Sort the tokens' assignments by expert: (offsets, slot, source).
+
+    ``ids`` is (tokens, topk) int32 or int64, as a router's topk gives it; an id
+    outside [0, experts) goes to no expert (padding, or an expert on another
+    GPU).  ``offsets`` (experts + 1): expert e owns the sorted rows
+    [offsets[e], offsets[e + 1]).  ``slot`` (tokens, topk): the sorted row of an
+    assignment, -1 where no expert takes it.  ``source`` (tokens * topk): the
+    assignment (token * topk + j) of every sorted row, followed by those that
+    no expert takes.  All int32; the sort is stable.
+    """
+    lib = load_library()
+    if not ids.is_cuda or ids.dim() != 2 or ids.dtype not in (torch.int32, torch.int64):
+        raise MuonError("ids must be a 2-D int32 or int64 CUDA tensor")
+    tokens, topk = ids.shape
+    need = int(lib.muon_expert_sort_workspace_size(tokens, topk, experts))
+    if need == 0:
+        raise MuonError(f"cannot sort {tokens} x {topk} assignments to {experts} experts (workspace query returned 0)")
+    ld = _pitch(ids, "ids")
+    device = ids.device
+
+    def call(handle):
+        # one allocation: offsets, slot and source, each from a 16-byte boundary
+        n, o = tokens * topk, (experts + 4) // 4 * 4
+        p = (n + 3) // 4 * 4
+        out = torch.empty(o + p + n, dtype=torch.int32, device=device)
+        offsets, slot, source = out[:experts + 1], out[o:o + n].view(tokens, topk), out[o + p:]
+        ws = workspace
+        if ws is None and need > 256:
+            ws = torch.empty(need, dtype=torch.uint8, device=device)
+        base = out.data_ptr()
+        _raise(lib.muon_expert_sort(ids.data_ptr(), ids.element_size(), ld, tokens, topk, experts, base, base + 4 * o,
+                                    base + 4 * (o + p), None if ws is None else ws.data_ptr(),
+                                    0 if ws is None else ws.numel() * ws.element_size(), handle), "muon_expert_sort")
+        return offsets, slot, source
+
+    return _on(device, stream, call)
+
+
+def muon_expert_gather(x: torch.Tensor, slot: torch.Tensor, *, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Lay the tokens' rows out by expert: out[slot[t, j]] = x[t].
+
+    ``x`` is (tokens, cols), ``slot`` as from muon_expert_sort.  ``out`` (rows,
+    cols) defaults to a new tensor of one row per assignment; rows that no slot
+    names keep their contents, and slots outside it are skipped.
+    """
+    lib = load_library()
+    tokens, topk = _slot_arg(slot, x.device)
+    ld = _rows_arg(x, "x", shape=(tokens, x.shape[-1]))
+    cols, dt = x.shape[1], _dtype_code(x.dtype)
+    ld_out = cols if out is None else _rows_arg(out, "out", x.device, x.dtype, (out.shape[0], cols))
+
+    def call(handle):
+        xs = torch.empty(tokens * topk, cols, dtype=x.dtype, device=x.device) if out is None else out
+        _raise(lib.muon_expert_gather(x.data_ptr(), ld, slot.data_ptr(), tokens, topk, cols, dt, xs.data_ptr(), ld_out,
+                                      xs.shape[0], handle), "muon_expert_gather")
+        return xs
+
+    return _on(x.device, stream, call)
+
+
+def muon_expert_combine(ys: torch.Tensor, slot: torch.Tensor, weights: torch.Tensor | None = None, *,
+                        out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Bring sorted rows back to their tokens: out[t] = sum_j weights[t, j] * ys[slot[t, j]].
+
+    ``weights`` is (tokens, topk) of any supported type (None: ones).  An
+    assignment that no expert takes adds nothing, whatever its weight.
+    """
+    lib = load_library()
+    tokens, topk = _slot_arg(slot, ys.device)
+    ld = _rows_arg(ys, "ys")
+    rows, cols = ys.shape
+    dt = _dtype_code(ys.dtype)
+    wdt = 0 if weights is None else _weights_arg(weights, slot)
+    ld_out = cols if out is None else _rows_arg(out, "out", ys.device, ys.dtype, (tokens, cols))
+
+    def call(handle):
+        y = torch.empty(tokens, cols, dtype=ys.dtype, device=ys.device) if out is None else out
+        _raise(lib.muon_expert_combine(ys.data_ptr(), ld, rows, slot.data_ptr(),
+                                       None if weights is None else weights.data_ptr(), wdt, tokens, topk, cols, dt,
+                                       y.data_ptr(), ld_out, handle), "muon_expert_combine")
+        return y
+
+    return _on(ys.device, stream, call)
+
+
+def muon_expert_gather_backward(dxs: torch.Tensor, slot: torch.Tensor, *, out: torch.Tensor | None = None,
+                                stream=None) -> torch.Tensor:
+    """The gradient of muon_expert_gather: out[t] = sum_j dxs[slot[t, j]]."""
+    return muon_expert_combine(dxs, slot, None, out=out, stream=stream)
+
+
+def muon_expert_combine_backward(dy: torch.Tensor, ys: torch.Tensor, slot: torch.Tensor,
+                                 weights: torch.Tensor | None = None, *, out: torch.Tensor | None = None, stream=None):
+    """The gradients of muon_expert_combine, (dys, dweights):
+    dys[slot[t, j]] = weights[t, j] * dy[t] and dweights[t, j] = <dy[t], ys[slot[t, j]]>.
+
+    ``out`` takes dys (a new tensor of ys's shape if None; rows that no slot
+    names keep their contents).  dweights has the weights' type, zero where no
+    expert takes the assignment; None if ``weights`` is None.
+    """
+    lib = load_library()
+    tokens, topk = _slot_arg(slot, ys.device)
+    ld_ys = _rows_arg(ys, "ys")
+    rows, cols = ys.shape
+    dt = _dtype_code(ys.dtype)
+    ld_dy = _rows_arg(dy, "dy", ys.device, ys.dtype, (tokens, cols))
+    wdt = 0 if weights is None else _weights_arg(weights, slot)
+    ld_out = cols if out is None else _rows_arg(out, "out", ys.device, ys.dtype, (rows, cols))
+
+    def call(handle):
+        dys = torch.empty(rows, cols, dtype=ys.dtype, device=ys.device) if out is None else out
+        dw = None if weights is None else torch.empty_like(weights)
+        _raise(lib.muon_expert_combine_backward(dy.data_ptr(), ld_dy, ys.data_ptr(), ld_ys, rows, slot.data_ptr(),
+                                                None if weights is None else weights.data_ptr(), wdt, tokens, topk,
+                                                cols, dt, dys.data_ptr(), ld_out, None if dw is None else dw.data_ptr(),
+                                                handle), "muon_expert_combine_backward")
+        return dys, dw
+
+    return _on(ys.device, stream, call)
+
+
+def _offsets_arg(offsets: torch.Tensor, device) -> int:
+    if not offsets.is_cuda or offsets.device != device or offsets.dtype != torch.int32 or offsets.dim() != 1 or \
+            not offsets.is_contiguous() or offsets.numel() < 2:
+        raise MuonError("offsets must be a contiguous int32 tensor of experts + 1 entries on the rows' device")
+    return offsets.numel() - 1
+
+
+def _stack_arg(w: torch.Tensor, name: str, experts: int, device, dtype=None):
+    """(outer, inner, row pitch, expert stride) of an (experts, outer, inner) stack."""
+    if not w.is_cuda or w.device != device or w.dim() != 3 or w.shape[0] != experts:
+        raise MuonError(f"{name} must be ({experts}, outer, inner) on {device}")
+    if dtype is not None and w.dtype != dtype:
+        raise MuonError(f"{name} must be {dtype}, not {w.dtype}")
+    return w.shape[1], w.shape[2], _pitch(w, name), w.stride(0) if experts > 1 else w.shape[1] * w.shape[2]
+
+
+def _status_arg(status, device):
+    if status is None:
+        return None
+    if not status.is_cuda or status.device != device or status.dtype != torch.int32 or status.numel() != 1:
+        raise MuonError("status must be one int32 word on the rows' device")
+    return status.data_ptr()
+
+
+def _expert_rows_product(entry, a, w, offsets, out, status, stream, to_outer):
+    """y = W xs (to_outer) or dxs = W^T dys, for every expert's rows."""
+    lib = load_library()
+    name = "xs" if to_outer else "dys"
+    ld_a = _rows_arg(a, name)
+    rows, width = a.shape
+    experts = _offsets_arg(offsets, a.device)
+    outer, inner, ld_w, stride_w = _stack_arg(w, "w", experts, a.device, a.dtype)
+    if width != (inner if to_outer else outer):
+        raise MuonError(f"{name} must have {inner if to_outer else outer} columns, not {width}")
+    cols, dt = (outer if to_outer else inner), _dtype_code(a.dtype)
+    ld_out = cols if out is None else _rows_arg(out, "out", a.device, a.dtype, (rows, cols))
+    word = _status_arg(status, a.device)
+
+    def call(handle):
+        d = torch.empty(rows, cols, dtype=a.dtype, device=a.device) if out is None else out
+        _raise(getattr(lib, entry)(a.data_ptr(), ld_a, w.data_ptr(), ld_w, stride_w, offsets.data_ptr(), experts, rows,
+                                   inner, outer, dt, d.data_ptr(), ld_out, word, handle), entry)
+        return d
+
+    return _on(a.device, stream, call)
+
+
+def muon_expert_product(xs: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, *, out: torch.Tensor | None = None,
+                        status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Every expert's rows times its weights: out[p] = w[e] @ xs[p] for the rows
+    p of expert e, offsets[e] <= p < offsets[e + 1].
+
+    ``xs`` is (rows, inner), ``w`` (experts, outer, inner) of the same type, both
+    with contiguous rows and any other strides; ``offsets`` as from
+    muon_expert_sort, read on the device.  Rows of ``out`` (rows, outer) that no
+    expert owns keep their contents.  bf16 and fp16 run on the tensor cores
+    where bases and strides are multiples of 16 bytes; fp32, and what TMA cannot
+    address, on the CUDA cores.  ``status``: one int32 word for a device-side
+    timeout.
+    """
+    return _expert_rows_product("muon_expert_product", xs, w, offsets, out, status, stream, True)
+
+
+def muon_expert_input_grad(dys: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, *,
+                           out: torch.Tensor | None = None, status: torch.Tensor | None = None,
+                           stream=None) -> torch.Tensor:
+    """The input gradient of muon_expert_product: out[p] = w[e]^T @ dys[p] for expert e's rows p."""
+    return _expert_rows_product("muon_expert_input_grad", dys, w, offsets, out, status, stream, False)
+
+
+def muon_expert_weight_grad(dys: torch.Tensor, xs: torch.Tensor, offsets: torch.Tensor, *,
+                            out: torch.Tensor | None = None, out_dtype: torch.dtype | None = None,
+                            accumulate: bool = False, status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """The weight gradients of muon_expert_product, (experts, outer, inner):
+    dW[e] = sum of dys[p]^T xs[p] over expert e's rows, zero without rows.
+
+    ``out_dtype`` (or ``out``'s type) is the operands' or float32; the stack's
+    matrices are gradients as muon_step and muon_step_blocks take them.
+    ``accumulate`` adds to a float32 ``out`` (gradient accumulation).
+    """
+    lib = load_library()
+    ld_dys = _rows_arg(dys, "dys")
+    rows, outer = dys.shape
+    ld_xs = _rows_arg(xs, "xs", dys.device, dys.dtype, (rows, xs.shape[-1]))
+    inner, dt = xs.shape[1], _dtype_code(dys.dtype)
+    experts = _offsets_arg(offsets, dys.device)
+    if accumulate and out is None:
+        raise MuonError("accumulate needs out")
+    if out is not None:
+        if out_dtype not in (None, out.dtype):
+            raise MuonError(f"out is {out.dtype}, out_dtype {out_dtype}")
+        if tuple(out.shape) != (experts, outer, inner):
+            raise MuonError(f"out must be {(experts, outer, inner)}, not {tuple(out.shape)}")
+        _, _, ld_out, stride_out = _stack_arg(out, "out", experts, dys.device)
+        out_dtype = out.dtype
+    else:
+        out_dtype = out_dtype or dys.dtype
+        ld_out, stride_out = inner, outer * inner
+    odt = _dtype_code(out_dtype)
+    word = _status_arg(status, dys.device)
+
+    def call(handle):
+        dw = torch.empty(experts, outer, inner, dtype=out_dtype, device=dys.device) if out is None else out
+        _raise(lib.muon_expert_weight_grad(dys.data_ptr(), ld_dys, xs.data_ptr(), ld_xs, offsets.data_ptr(), experts,
+                                           rows, inner, outer, dt, dw.data_ptr(), ld_out, stride_out, odt,
+                                           int(accumulate), word, handle), "muon_expert_weight_grad")
+        return dw
+
+    return _on(dys.device, stream, call)
+
+
+class ExpertMuonStep:
+    """A Muon step of expert stacks straight from the sorted tokens, without
+    holding all of their gradients.
+
+    ``params`` and ``moms`` are lists of (experts, outer, inner) stacks; a call
+    takes, per stack, the (dys, xs, offsets) of its product's backward pass.  The
+    experts are taken in slices whose gradients fit ``slice_bytes``: the slice's
+    weight gradients go into one buffer that all slices share, and the block
+    step on the slice consumes them, so a call needs that buffer and one
+    workspace instead of a gradient per parameter.  The result is that of
+    muon_expert_weight_grad followed by muon_step_blocks.  ``grad_dtype``: the
+    buffer's type, the operands' (default: each stack's own) or float32.
+    ``blocks`` as for muon_step_blocks, one entry per stack.
+    """
+
+    def __init__(self, params, moms, *, blocks: Sequence | None = None, slice_bytes: int = 512 << 20,
+                 grad_dtype: torch.dtype | None = None, **hp):
+        if len(params) == 0 or len(params) != len(moms):
+            raise MuonError("params and moms must be non-empty lists of equal length")
+        blocks = [None] * len(params) if blocks is None else list(blocks)
+        if len(blocks) != len(params):
+            raise MuonError("blocks must have one entry per parameter")
+        for w in params:
+            if not w.is_cuda or w.dim() != 3 or w.device != params[0].device:
+                raise MuonError("params must be (experts, outer, inner) stacks on one device")
+        self.device = params[0].device
+        self.shapes = [tuple(w.shape) for w in params]
+        dtypes = [grad_dtype or w.dtype for w in params]
+        self.slices = []  # (stack, first expert, last expert)
+        most = 0
+        for i, w in enumerate(params):
+            one = w.shape[1] * w.shape[2] * dtypes[i].itemsize
+            per = max(1, min(w.shape[0], slice_bytes // one))
+            self.slices += [(i, e, min(e + per, w.shape[0])) for e in range(0, w.shape[0], per)]
+            most = max(most, per * one)
+        self._buffer = torch.empty(most, dtype=torch.uint8, device=self.device)
+        self.grads, self.steps = [], []
+        for i, e0, e1 in self.slices:
+            shape = (e1 - e0,) + self.shapes[i][1:]
+            n = shape[0] * shape[1] * shape[2] * dtypes[i].itemsize
+            self.grads.append(self._buffer[:n].view(dtypes[i]).view(shape))
+            self.steps.append(MuonStep([params[i][e0:e1]], [self.grads[-1]], [moms[i][e0:e1]], blocks=[blocks[i]],
+                                       workspace_bytes=1, **hp))
+        self.workspace = torch.empty(max(s.workspace_needed[1] for s in self.steps), dtype=torch.uint8,
+                                     device=self.device)
+        for step in self.steps:
+            step.workspace = self.workspace
+
+    def __call__(self, factors, stream=None) -> None:
+        if len(factors) != len(self.shapes):
+            raise MuonError("factors must have one (dys, xs, offsets) per stack")
+        for (experts, outer, inner), (dys, xs, offsets) in zip(self.shapes, factors):
+            if offsets.numel() != experts + 1 or dys.shape[-1] != outer or xs.shape[-1] != inner:
+                raise MuonError("a stack's dys, xs and offsets do not fit its experts x outer x inner")
+
+        def call(handle):
+            for (i, e0, e1), grad, step in zip(self.slices, self.grads, self.steps):
+                dys, xs, offsets = factors[i]
+                muon_expert_weight_grad(dys, xs, offsets[e0:e1 + 1], out=grad)
+                step(stream=handle)
+
+        _on(self.device, stream, call)
+
+    @property
+    def status(self) -> torch.Tensor:
+        """The blocks' status words, in the order of the stacks, their experts and blocks."""
+        return torch.cat([s.status_in_param_order() for s in self.steps])

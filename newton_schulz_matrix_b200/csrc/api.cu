@@ -26,8 +26,14 @@
 #include "../../include/muon.h"
 #include "common.cuh"
 #include "internal.h"
+#include "profile.h"
 
 using namespace muon;
+
+Profiler& muon::profiler() {
+  static Profiler p;
+  return p;
+}
 
 namespace {
 
@@ -36,53 +42,13 @@ inline size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 inline int round8(int v) { return (v + 7) / 8 * 8; }
 
 // ------------------------------------------------------------------ profiler
-enum ProfKind {
-  kProfPack, kProfNorm, kProfSyrkTc, kProfGemmTc, kProfGemmSimt, kProfUnpack, kProfFusedSmall, kProfTf32, kProfChain,
-  kProfStatus, kProfSplit, kProfKinds
-};
 // product kinds cover both tensor-core kernels (gemm_pair_kernel for M >= 256, gemm_kernel below);
 // tc_chain is a whole chain in one launch (gemm_chain_kernel)
 const char* const kProfNames[kProfKinds] = {"pack_kernel", "norm_kernel", "tc_product[symmetric]", "tc_product",
                                             "gemm_simt_kernel", "unpack_kernel", "ns_fused_small_kernel",
                                             "tc_product[3xtf32]", "tc_chain", "status_or_kernel",
-                                            "split_tf32_kernel"};
-struct ProfRec {
-  int kind;
-  cudaEvent_t a, b;
-  double flops, exec_flops, bytes;
-};
-struct Profiler {
-  bool on = false;
-  std::vector<ProfRec> recs;
-  std::mutex mu;
-};
-Profiler& profiler() {
-  static Profiler p;
-  return p;
-}
-// Brackets one launch with events on its stream while profiling is on.
-struct ProfScope {
-  ProfRec rec{};
-  bool active = false;
-  cudaStream_t s;
-  ProfScope(int kind, double flops, double bytes, cudaStream_t st, double exec_flops = -1.0) : s(st) {
-    Profiler& P = profiler();
-    if (!P.on) return;
-    rec.kind = kind; rec.flops = flops; rec.bytes = bytes;
-    rec.exec_flops = exec_flops < 0.0 ? flops : exec_flops;
-    if (cudaEventCreate(&rec.a) != cudaSuccess) return;
-    if (cudaEventCreate(&rec.b) != cudaSuccess) { cudaEventDestroy(rec.a); return; }
-    cudaEventRecord(rec.a, s);
-    active = true;
-  }
-  ~ProfScope() {
-    if (!active) return;
-    cudaEventRecord(rec.b, s);
-    Profiler& P = profiler();
-    std::lock_guard<std::mutex> g(P.mu);
-    P.recs.push_back(rec);
-  }
-};
+                                            "split_tf32_kernel", "expert_sort", "expert_gather", "expert_combine",
+                                            "expert_combine_backward", "expert_product", "expert_product_simt"};
 
 struct Seg {          // `count` matrices of one caller group, starting at index `first`
   int group, first, count;
@@ -205,7 +171,18 @@ Bufs carve(const Layout& L, int chunk, void* ws) {
   return B;
 }
 
-std::vector<Batch> plan_groups(const muon_group* groups, int n_groups) {
+// What the planner, the pack and the update need of one caller group.
+struct GroupView {
+  int rows, cols, count;
+  int src_dtype, dst_dtype;
+  long long ld_src, ld_mom, ld_dst;  // row pitches in elements
+  const void* const* src;  // G (step) or X (orthogonalisation alone)
+  float* const* mom;       // M, or null
+  void* const* dst;        // W or X
+};
+
+std::vector<Batch> plan_groups(const std::vector<GroupView>& groups) {
+  const int n_groups = (int)groups.size();
   std::vector<Batch> out;
   for (int g = 0; g < n_groups; ++g) {
     const int n = std::min(groups[g].rows, groups[g].cols), m = std::max(groups[g].rows, groups[g].cols);
@@ -623,15 +600,18 @@ int run_chain_launch(const Ctx& c, const Layout& L, const Bufs& B, int chunk, co
 }
 
 // ------------------------------------------------------------------ driver
-struct SrcView {      // what the pack / unpack kernels need for one caller group
-  int rows, cols;
-  int src_dtype, dst_dtype;
-  const void* const* src;
-  float* const* mom;
-  void* const* dst;
-};
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
-int run_batches(const std::vector<Batch>& batches, const std::vector<SrcView>& views, const std::vector<long long>& first_index,
+// Whether every row of these matrices starts on a 16-byte boundary (the
+// vector path of the pack and update kernels).
+bool rows16(const void* const* p, int count, long long ld, int dtype) {
+  if (ld * dtype_size(dtype) % 16 != 0) return false;
+  for (int i = 0; i < count; ++i)
+    if (!aligned16(p[i])) return false;
+  return true;
+}
+
+int run_batches(const std::vector<Batch>& batches, const std::vector<GroupView>& views, const std::vector<long long>& first_index,
                 const muon_ns_params* ns, bool update, float mu, int nesterov, float lr, float wd, float scale_coef,
                 void* ws, size_t ws_bytes, int* status, cudaStream_t s) {
   for (const Batch& bt : batches) {
@@ -676,7 +656,7 @@ int run_batches(const std::vector<Batch>& batches, const std::vector<SrcView>& v
       const int pack_dt = ns->compute_dtype == MUON_FP32 ? MUON_FP32 : (prescale ? MUON_FP16 : MUON_BF16);
       auto launch_pieces = [&](int pass) {
         for (const Piece& pc : pieces) {
-          const SrcView& v = views[pc.group];
+          const GroupView& v = views[pc.group];
           SegmentPtrs ptrs;
           for (int i = 0; i < pc.count; ++i) {
             ptrs.src[i] = v.src[pc.first + i];
@@ -685,6 +665,9 @@ int run_batches(const std::vector<Batch>& batches, const std::vector<SrcView>& v
           }
           PackArgs a{};
           a.rows = v.rows; a.cols = v.cols; a.count = pc.count;
+          a.ld_src = v.ld_src; a.ld_mom = v.ld_mom;
+          a.vec = rows16(ptrs.src, pc.count, v.ld_src, v.src_dtype) &&
+                  (v.mom == nullptr || rows16(reinterpret_cast<const void* const*>(ptrs.mom), pc.count, v.ld_mom, MUON_FP32));
           a.src_dtype = v.src_dtype; a.x_dtype = pack_dt;
           a.momentum_mode = update ? 1 : 0; a.mu = mu; a.nesterov = nesterov;
           a.x = reinterpret_cast<char*>(B.X[0]) + (size_t)pc.slot * B.x_bs * L.x_es;
@@ -726,11 +709,14 @@ int run_batches(const std::vector<Batch>& batches, const std::vector<SrcView>& v
         us.step = lr * scale_coef * std::sqrt((float)bt.m);  // max(rows, cols) = m for every matrix of the batch
         us.status = status;
         for (const Piece& pc : pieces) {
-          const SrcView& v = views[pc.group];
+          const GroupView& v = views[pc.group];
+          const bool pitch16 = v.ld_dst * dtype_size(v.dst_dtype) % 16 == 0;
           for (int i = 0; i < pc.count; ++i) {
             us.w[pc.slot + i] = v.dst[pc.first + i];
+            us.ld[pc.slot + i] = (int)v.ld_dst;
             us.status_idx[pc.slot + i] = (int)(first_index[pc.group] + pc.first + i);
-            us.kind[pc.slot + i] = (unsigned char)((v.rows > v.cols ? 1 : 0) | (v.dst_dtype << 1));
+            us.kind[pc.slot + i] = (unsigned char)((v.rows > v.cols ? 1 : 0) | (v.dst_dtype << 1) |
+                                                   (pitch16 && aligned16(v.dst[pc.first + i]) ? 8 : 0));
           }
         }
         if (run_chain_launch(ctx, L, B, chunk, ns, prescale, &xi, &out_dt, &us) != 0) return MUON_ERR_CUDA;
@@ -745,7 +731,7 @@ int run_batches(const std::vector<Batch>& batches, const std::vector<SrcView>& v
       }
       if (run_chain_launch(ctx, L, B, chunk, ns, prescale, &xi, &out_dt, nullptr) != 0) return MUON_ERR_CUDA;
       for (const Piece& pc : pieces) {
-        const SrcView& v = views[pc.group];
+        const GroupView& v = views[pc.group];
         SegmentPtrs ptrs;
         for (int i = 0; i < pc.count; ++i) {
           ptrs.src[i] = nullptr;
@@ -754,6 +740,8 @@ int run_batches(const std::vector<Batch>& batches, const std::vector<SrcView>& v
         }
         UnpackArgs u{};
         u.rows = v.rows; u.cols = v.cols; u.count = pc.count;
+        u.ld_dst = v.ld_dst;
+        u.vec = rows16(ptrs.dst, pc.count, v.ld_dst, v.dst_dtype);
         u.dst_dtype = v.dst_dtype; u.x_dtype = out_dt;
         u.update_mode = update ? 1 : 0;
         u.decay = 1.f - lr * wd;
@@ -773,15 +761,16 @@ int run_batches(const std::vector<Batch>& batches, const std::vector<SrcView>& v
   return MUON_OK;
 }
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
-
-int check_groups(const muon_group* groups, int n_groups, const muon_hparams* hp, long long* total) {
-  if (!groups || n_groups <= 0 || !hp) return MUON_ERR_INVALID;
-  if (!ns_params_ok(&hp->ns)) return MUON_ERR_INVALID;
+int check_hparams(const muon_hparams* hp) {
+  if (!hp || !ns_params_ok(&hp->ns)) return MUON_ERR_INVALID;
   if (!std::isfinite(hp->lr) || !std::isfinite(hp->momentum) || !std::isfinite(hp->weight_decay) ||
       !std::isfinite(hp->scale_coef))
     return MUON_ERR_INVALID;
-  long long t = 0;
+  return MUON_OK;
+}
+
+int check_groups(const muon_group* groups, int n_groups, const muon_hparams* hp, std::vector<GroupView>* views) {
+  if (!groups || n_groups <= 0 || check_hparams(hp) != MUON_OK) return MUON_ERR_INVALID;
   for (int g = 0; g < n_groups; ++g) {
     const muon_group& G = groups[g];
     if (G.rows <= 0 || G.cols <= 0 || G.count < 0) return MUON_ERR_INVALID;
@@ -792,9 +781,38 @@ int check_groups(const muon_group* groups, int n_groups, const muon_hparams* hp,
       if (!G.W[i] || !G.G[i] || !G.M[i]) return MUON_ERR_INVALID;
       if (!aligned16(G.W[i]) || !aligned16(G.G[i]) || !aligned16(G.M[i])) return MUON_ERR_INVALID;
     }
-    t += G.count;
+    views->push_back(GroupView{G.rows, G.cols, G.count, G.g_dtype, G.w_dtype, G.cols, G.cols, G.cols, G.G, G.M, G.W});
   }
-  *total = t;
+  return MUON_OK;
+}
+
+// The largest row pitch of a block: offsets inside a matrix stay far below
+// 2^63 and the pitch fits the update slots' 32-bit words.
+constexpr long long kMaxPitch = 0x7fffffffLL;
+
+bool element_aligned(const void* p, int dtype) {
+  return reinterpret_cast<uintptr_t>(p) % (uintptr_t)dtype_size(dtype) == 0;
+}
+
+int check_block_groups(const muon_block_group* groups, int n_groups, const muon_hparams* hp,
+                       std::vector<GroupView>* views) {
+  if (!groups || n_groups <= 0 || check_hparams(hp) != MUON_OK) return MUON_ERR_INVALID;
+  for (int g = 0; g < n_groups; ++g) {
+    const muon_block_group& G = groups[g];
+    if (G.rows <= 0 || G.cols <= 0 || G.count < 0) return MUON_ERR_INVALID;
+    if ((long long)G.rows * G.cols > (1LL << 34)) return MUON_ERR_INVALID;
+    if (!dtype_ok(G.w_dtype) || !dtype_ok(G.g_dtype)) return MUON_ERR_UNSUPPORTED;
+    for (const long long ld : {G.ld_w, G.ld_g, G.ld_m})
+      if (ld < G.cols || ld > kMaxPitch) return MUON_ERR_INVALID;
+    if (G.count > 0 && (!G.W || !G.G || !G.M)) return MUON_ERR_INVALID;
+    for (int i = 0; i < G.count; ++i) {
+      if (!G.W[i] || !G.G[i] || !G.M[i]) return MUON_ERR_INVALID;
+      if (!element_aligned(G.W[i], G.w_dtype) || !element_aligned(G.G[i], G.g_dtype) ||
+          !element_aligned(G.M[i], MUON_FP32))
+        return MUON_ERR_INVALID;
+    }
+    views->push_back(GroupView{G.rows, G.cols, G.count, G.g_dtype, G.w_dtype, G.ld_g, G.ld_m, G.ld_w, G.G, G.M, G.W});
+  }
   return MUON_OK;
 }
 
@@ -805,6 +823,24 @@ size_t ws_for(const std::vector<Batch>& batches, const muon_ns_params* ns, bool 
     best = std::max(best, chunk_bytes(L, full ? b.total : 1));
   }
   return best;
+}
+
+// One step over checked groups (muon_step and muon_step_blocks).
+int step_views(const std::vector<GroupView>& views, const muon_hparams* hp, void* ws, size_t ws_bytes, int* status,
+               cudaStream_t s) {
+  if (!ws || (reinterpret_cast<uintptr_t>(ws) & (kAlign - 1))) return MUON_ERR_INVALID;
+  std::vector<Batch> batches = plan_groups(views);
+  if (ws_bytes < ws_for(batches, &hp->ns, false)) return MUON_ERR_WORKSPACE;
+  std::vector<long long> first;
+  long long total = 0;
+  for (const GroupView& v : views) {
+    first.push_back(total);
+    total += v.count;
+  }
+  if (status && total > 0 && cudaMemsetAsync(status, 0, (size_t)total * sizeof(int), s) != cudaSuccess)
+    return MUON_ERR_CUDA;
+  return run_batches(batches, views, first, &hp->ns, true, hp->momentum, hp->nesterov, hp->lr, hp->weight_decay,
+                     hp->scale_coef, ws, ws_bytes, status, s);
 }
 
 double flops_of(int rows, int cols, const muon_ns_params* ns) {
@@ -841,39 +877,55 @@ double flops_of(int rows, int cols, const muon_ns_params* ns) {
 extern "C" {
 
 size_t muon_workspace_size(const muon_group* groups, int n_groups, const muon_hparams* hp) {
-  long long total = 0;
-  if (check_groups(groups, n_groups, hp, &total) != MUON_OK) return 0;
-  return ws_for(plan_groups(groups, n_groups), &hp->ns, true);
+  std::vector<GroupView> views;
+  if (check_groups(groups, n_groups, hp, &views) != MUON_OK) return 0;
+  return ws_for(plan_groups(views), &hp->ns, true);
 }
 
 size_t muon_workspace_min(const muon_group* groups, int n_groups, const muon_hparams* hp) {
-  long long total = 0;
-  if (check_groups(groups, n_groups, hp, &total) != MUON_OK) return 0;
-  return ws_for(plan_groups(groups, n_groups), &hp->ns, false);
+  std::vector<GroupView> views;
+  if (check_groups(groups, n_groups, hp, &views) != MUON_OK) return 0;
+  return ws_for(plan_groups(views), &hp->ns, false);
 }
 
 int muon_step(const muon_group* groups, int n_groups, const muon_hparams* hp, void* ws, size_t ws_bytes,
               int* status_per_matrix, void* stream) {
-  long long total = 0;
-  int rc = check_groups(groups, n_groups, hp, &total);
+  std::vector<GroupView> views;
+  const int rc = check_groups(groups, n_groups, hp, &views);
   if (rc != MUON_OK) return rc;
-  if (!ws || (reinterpret_cast<uintptr_t>(ws) & (kAlign - 1))) return MUON_ERR_INVALID;
-  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  std::vector<Batch> batches = plan_groups(groups, n_groups);
-  if (ws_bytes < ws_for(batches, &hp->ns, false)) return MUON_ERR_WORKSPACE;
-  std::vector<SrcView> views(n_groups);
-  std::vector<long long> first(n_groups);
-  long long acc = 0;
-  for (int g = 0; g < n_groups; ++g) {
-    views[g] = SrcView{groups[g].rows, groups[g].cols, groups[g].g_dtype, groups[g].w_dtype,
-                       groups[g].G, groups[g].M, groups[g].W};
-    first[g] = acc;
-    acc += groups[g].count;
+  return step_views(views, hp, ws, ws_bytes, status_per_matrix, reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t muon_blocks_workspace_size(const muon_block_group* groups, int n_groups, const muon_hparams* hp) {
+  try {
+    std::vector<GroupView> views;
+    if (check_block_groups(groups, n_groups, hp, &views) != MUON_OK) return 0;
+    return ws_for(plan_groups(views), &hp->ns, true);
+  } catch (...) {  // std::bad_alloc: no exception crosses the C ABI
+    return 0;
   }
-  if (status_per_matrix && total > 0 && cudaMemsetAsync(status_per_matrix, 0, (size_t)total * sizeof(int), s) != cudaSuccess)
-    return MUON_ERR_CUDA;
-  return run_batches(batches, views, first, &hp->ns, true, hp->momentum, hp->nesterov, hp->lr, hp->weight_decay,
-                     hp->scale_coef, ws, ws_bytes, status_per_matrix, s);
+}
+
+size_t muon_blocks_workspace_min(const muon_block_group* groups, int n_groups, const muon_hparams* hp) {
+  try {
+    std::vector<GroupView> views;
+    if (check_block_groups(groups, n_groups, hp, &views) != MUON_OK) return 0;
+    return ws_for(plan_groups(views), &hp->ns, false);
+  } catch (...) {  // std::bad_alloc: no exception crosses the C ABI
+    return 0;
+  }
+}
+
+int muon_step_blocks(const muon_block_group* groups, int n_groups, const muon_hparams* hp, void* ws, size_t ws_bytes,
+                     int* status_per_block, void* stream) {
+  try {
+    std::vector<GroupView> views;
+    const int rc = check_block_groups(groups, n_groups, hp, &views);
+    if (rc != MUON_OK) return rc;
+    return step_views(views, hp, ws, ws_bytes, status_per_block, reinterpret_cast<cudaStream_t>(stream));
+  } catch (...) {  // std::bad_alloc: no exception crosses the C ABI
+    return MUON_ERR_INVALID;
+  }
 }
 
 size_t muon_ns_workspace_size(int count, int rows, int cols, const muon_ns_params* ns) {
@@ -895,7 +947,8 @@ int muon_ns_batched(void* const* X, int count, int rows, int cols, int dtype, co
   Batch b{std::min(rows, cols), std::max(rows, cols), {Seg{0, 0, count}}, count};
   std::vector<Batch> batches{b};
   if (ws_bytes < ws_for(batches, ns, false)) return MUON_ERR_WORKSPACE;
-  std::vector<SrcView> views{SrcView{rows, cols, dtype, dtype, const_cast<const void* const*>(X), nullptr, X}};
+  std::vector<GroupView> views{GroupView{rows, cols, count, dtype, dtype, cols, cols, cols,
+                                         const_cast<const void* const*>(X), nullptr, X}};
   std::vector<long long> first{0};
   if (status_per_matrix && cudaMemsetAsync(status_per_matrix, 0, (size_t)count * sizeof(int), s) != cudaSuccess)
     return MUON_ERR_CUDA;

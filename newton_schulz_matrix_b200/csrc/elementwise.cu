@@ -125,7 +125,7 @@ pack_kernel(const PackArgs a, const __grid_constant__ SegmentPtrs p) {
   float* mom = MOMENTUM ? p.mom[b] : nullptr;
   TX* x = reinterpret_cast<TX*>(a.x) + (long long)b * a.x_batch_stride;
 
-  const bool full = (r0 + kTile <= a.rows) && (c0 + kTile <= a.cols) && (a.cols % 8 == 0);
+  const bool full = (r0 + kTile <= a.rows) && (c0 + kTile <= a.cols) && a.vec;
   const bool store = a.pass != 1;
   float u[4][4];  // [row pass][element]
   if (full) {
@@ -133,9 +133,9 @@ pack_kernel(const PackArgs a, const __grid_constant__ SegmentPtrs p) {
     float g[4][4], m[4][4];
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      const long long off = (long long)(r0 + q * 16 + lr) * a.cols + c0 + lc;
-      load4(src + off, g[q]);
-      if (MOMENTUM) load4(mom + off, m[q]);
+      const long long r = r0 + q * 16 + lr;
+      load4(src + r * a.ld_src + c0 + lc, g[q]);
+      if (MOMENTUM) load4(mom + r * a.ld_mom + c0 + lc, m[q]);
     }
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
@@ -145,7 +145,7 @@ pack_kernel(const PackArgs a, const __grid_constant__ SegmentPtrs p) {
           m[q][i] = a.mu * m[q][i] + (1.f - a.mu) * g[q][i];
           u[q][i] = a.nesterov ? (1.f - a.mu) * g[q][i] + a.mu * m[q][i] : m[q][i];
         }
-        if (store) store4(mom + (long long)(r0 + q * 16 + lr) * a.cols + c0 + lc, m[q]);
+        if (store) store4(mom + (long long)(r0 + q * 16 + lr) * a.ld_mom + c0 + lc, m[q]);
       } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i) u[q][i] = g[q][i];
@@ -160,9 +160,9 @@ pack_kernel(const PackArgs a, const __grid_constant__ SegmentPtrs p) {
         const int c = c0 + lc + i;
         u[q][i] = 0.f;
         if (r < a.rows && c < a.cols) {
-          const long long off = (long long)r * a.cols + c;
-          const float gv = to_f32(src[off]);
+          const float gv = to_f32(src[(long long)r * a.ld_src + c]);
           if (MOMENTUM) {
+            const long long off = (long long)r * a.ld_mom + c;
             const float mv = a.mu * mom[off] + (1.f - a.mu) * gv;
             if (store) mom[off] = mv;
             u[q][i] = a.nesterov ? (1.f - a.mu) * gv + a.mu * mv : mv;
@@ -266,9 +266,9 @@ unpack_kernel(const UnpackArgs a, const __grid_constant__ SegmentPtrs p) {
   const int lr = threadIdx.x >> 2, lc = (threadIdx.x & 3) * 16;
   const TX* __restrict__ x = reinterpret_cast<const TX*>(a.x) + (long long)b * a.x_batch_stride;
   TD* __restrict__ dst = reinterpret_cast<TD*>(p.dst[b]);
-  const bool full = (r0 + kTile <= a.rows) && (c0 + kTile <= a.cols) && (a.cols % 8 == 0);
+  const bool full = (r0 + kTile <= a.rows) && (c0 + kTile <= a.cols) && a.vec;
   const int r = r0 + lr;
-  const long long off = (long long)r * a.cols + c0 + lc;
+  const long long off = (long long)r * a.ld_dst + c0 + lc;
 
   // Both global loads (W and the orientated O) are issued before either is used,
   // so each thread waits for one memory round trip, not two.
@@ -315,7 +315,7 @@ unpack_kernel(const UnpackArgs a, const __grid_constant__ SegmentPtrs p) {
     for (int i = 0; i < 16; ++i) {
       const int c = c0 + lc + i;
       if (c < a.cols) {
-        const long long o2 = (long long)r * a.cols + c;
+        const long long o2 = (long long)r * a.ld_dst + c;
         float v = UPDATE ? weight_update(to_f32(dst[o2]), o[i], a.decay, a.step) : o[i];
         dst[o2] = from_f32<TD>(v);
       }

@@ -20,6 +20,8 @@ struct SegmentPtrs {
 
 struct PackArgs {
   int rows, cols, count;
+  long long ld_src, ld_mom;  // row pitch of src and mom in elements (cols where they are dense)
+  int vec;              // 1: every row of src and mom starts on 16 bytes
   int src_dtype;        // G or X storage dtype
   int x_dtype;          // workspace dtype (bf16/fp16 tensor path, fp32 SIMT path)
   int momentum_mode;    // 1: M <- mu M + (1-mu) G, U = nesterov ? lerp : M;  0: U = src
@@ -45,6 +47,8 @@ void launch_norm(const float* partials, int partial_stride, int n_partials, int 
 
 struct UnpackArgs {
   int rows, cols, count;
+  long long ld_dst;     // row pitch of dst in elements (cols where it is dense)
+  int vec;              // 1: every row of dst starts on 16 bytes
   int dst_dtype;        // W or X storage dtype
   int x_dtype;
   int update_mode;      // 1: W <- decay W - step O;  0: X <- O
@@ -74,8 +78,9 @@ struct UpdateSlots {
   float decay, step;                // decay = 1 - lr wd, step = lr scale_coef sqrt(max(r, c))
   int* status;                      // per-matrix status words (may be null)
   void* w[kMax];                    // W of batch index b
+  int ld[kMax];                     // its row pitch in elements
   int status_idx[kMax];             // its index into status
-  unsigned char kind[kMax];         // bit 0: stored transposed (m x n); bits 1-2: W dtype
+  unsigned char kind[kMax];         // bit 0: stored transposed (m x n); bits 1-2: W dtype; bit 3: rows start on 16 bytes
 };
 
 // D[b] = epilogue(A[b] * op(B[b])) for b < batch, all row-major.

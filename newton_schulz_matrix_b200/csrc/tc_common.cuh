@@ -383,17 +383,16 @@ __device__ __forceinline__ WBox w_box(const Params& p, const Slots& u, const Til
   const int gj0 = t.tn * BN + chunk * 32;
   const unsigned kind = u.kind[t.b];
   WBox w;
-  w.wdt = (int)(kind >> 1);
+  w.wdt = (int)(kind >> 1) & 3;
+  w.ld = u.ld[t.b];
   w.es = w.wdt == kFP32 ? 4 : 2;
   char* W = reinterpret_cast<char*>(u.w[t.b]);
   if (!(kind & 1u)) {  // W is M x N like O
-    w.ld = p.N;
-    w.base = W + ((long long)gi_base * p.N + gj0) * w.es;
+    w.base = W + (gi_base * w.ld + gj0) * w.es;
     w.rows = min(32, p.M - gi_base);
     w.cols = min(32, p.N - gj0);
   } else {             // W is N x M: the box's rows are O's columns
-    w.ld = p.M;
-    w.base = W + ((long long)gj0 * p.M + gi_base) * w.es;
+    w.base = W + (gj0 * w.ld + gi_base) * w.es;
     w.rows = min(32, p.N - gj0);
     w.cols = min(32, p.M - gi_base);
   }
@@ -415,7 +414,7 @@ __device__ __forceinline__ WPrefetch prefetch_w(const Params& p, const Slots& u,
   const int gj0 = t.tn * BN + chunk * 32;
   if (gj0 + 32 > p.N || gi_base + 32 > p.M) return pf;  // ragged boxes load W as they go
   const WBox w = w_box(p, u, t, q, chunk);
-  if (w.wdt == kFP32 || (w.ld * 2) % 16 != 0) return pf;
+  if (w.wdt == kFP32 || !(u.kind[t.b] & 8u)) return pf;
 #pragma unroll
   for (int it = 0; it < 4; ++it)
     pf.q[it] = *reinterpret_cast<const uint4*>(w.base + ((long long)(it * 8 + (lane >> 2)) * w.ld + (lane & 3) * 8) * 2);
@@ -511,7 +510,7 @@ __device__ __forceinline__ void update_chunk(const Params& p, const Slots& u, co
   }
   __syncwarp();
   const WBox w = w_box(p, u, t, q, chunk);
-  const bool rows_vec = (w.ld * w.es) % 16 == 0;
+  const bool rows_vec = (u.kind[t.b] & 8u) != 0;
 #pragma unroll
   for (int it = 0; it < 4; ++it) {
     const int r = it * 8 + (lane >> 2);

@@ -1,0 +1,210 @@
+"""Host-only checks of the expert-layer operators and the block step: argument
+checks of the C ABI and of the binding, workspace sizes, without a GPU."""
+import ctypes
+
+import pytest
+import torch
+
+import newton_schulz_matrix_b200 as nsm
+
+P = 1 << 20  # a stand-in device pointer: nothing below launches
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from newton_schulz_matrix_b200 import build
+    build.build()
+    return nsm.load_library()
+
+
+def test_sort_refusals(lib):
+    size = lib.muon_expert_sort_workspace_size
+    assert size(32, 8, 216) > 0 and size(0, 1, 1) > 0
+    assert size(1 << 20, 8, 64) > 256  # several runs count apart
+    for bad in ((-1, 8, 64), (32, 0, 64), (32, 8, 0), (32, 8, nsm.EXPERT_MAX + 1), (1 << 30, 8, 64)):
+        assert size(*bad) == 0
+    ok = dict(ids=P, es=8, ld=8, tokens=1 << 17, topk=8, experts=64, offsets=P, slot=P, source=P, ws=P, bytes=0)
+    # the workspace is too small: every other argument is right
+    assert lib.muon_expert_sort(*ok.values(), None) == -3
+    for change, rc in ((dict(es=2), -2), (dict(ids=None), -1), (dict(ids=P + 4), -1), (dict(ld=7), -1), (dict(topk=0), -1),
+                       (dict(tokens=-1), -1), (dict(experts=0), -1), (dict(experts=2000), -1), (dict(offsets=None), -1),
+                       (dict(offsets=P + 2), -1), (dict(slot=P + 1), -1), (dict(source=None), -1), (dict(ws=None), -1),
+                       (dict(ws=P + 2), -1), (dict(tokens=1 << 29), -1)):
+        assert lib.muon_expert_sort(*dict(ok, **change).values(), None) == rc, change
+
+
+def test_route_refusals(lib):
+    gather = dict(x=P, ld_x=64, slot=P, tokens=4, topk=2, cols=64, dtype=0, xs=P, ld_xs=64, rows=8)
+    for change, rc in ((dict(ld_x=63), -1), (dict(x=None), -1), (dict(x=P + 1), -1), (dict(slot=None), -1),
+                       (dict(slot=P + 2), -1), (dict(topk=0), -1), (dict(cols=0), -1), (dict(tokens=-1), -1),
+                       (dict(dtype=3), -2), (dict(xs=P + 1), -1), (dict(ld_xs=10), -1), (dict(rows=-1), -1),
+                       (dict(rows=1 << 31), -1), (dict(dtype=2, x=P + 2), -1), (dict(tokens=1 << 30, topk=4), -1)):
+        assert lib.muon_expert_gather(*dict(gather, **change).values(), None) == rc, change
+    assert lib.muon_expert_gather(*dict(gather, tokens=0, slot=None, x=None).values(), None) == 0
+    combine = dict(ys=P, ld_ys=64, rows=8, slot=P, w=P, wdt=2, tokens=4, topk=2, cols=64, dtype=0, y=P, ld_y=64)
+    for change, rc in ((dict(ys=None), -1), (dict(ld_ys=1), -1), (dict(w=P + 2), -1), (dict(wdt=5), -2), (dict(y=None), -1),
+                       (dict(ld_y=0), -1), (dict(dtype=-1), -2), (dict(slot=None), -1)):
+        assert lib.muon_expert_combine(*dict(combine, **change).values(), None) == rc, change
+    back = dict(dy=P, ld_dy=64, ys=P, ld_ys=64, rows=8, slot=P, w=P, wdt=2, tokens=4, topk=2, cols=64, dtype=0, dys=P,
+                ld_dys=64, dw=P)
+    for change, rc in ((dict(dy=None), -1), (dict(ld_dy=2), -1), (dict(ys=None), -1), (dict(dys=None), -1),
+                       (dict(dw=P + 2), -1), (dict(w=None, wdt=9), -2), (dict(ld_dys=63), -1)):
+        assert lib.muon_expert_combine_backward(*dict(back, **change).values(), None) == rc, change
+
+
+def test_product_refusals(lib):
+    fwd = dict(xs=P, ld_xs=64, w=P, ld_w=64, stride_w=64 * 32, offsets=P, experts=4, rows=10, inner=64, outer=32, dtype=0,
+               y=P, ld_y=32, status=None)
+    for change, rc in ((dict(xs=None), -1), (dict(ld_xs=63), -1), (dict(w=P + 1), -1), (dict(ld_w=1), -1),
+                       (dict(stride_w=-1), -1), (dict(offsets=None), -1), (dict(offsets=P + 2), -1), (dict(experts=0), -1),
+                       (dict(experts=1025), -1), (dict(rows=-1), -1), (dict(inner=0), -1), (dict(outer=0), -1),
+                       (dict(dtype=4), -2), (dict(y=None), -1), (dict(ld_y=31), -1)):
+        assert lib.muon_expert_product(*dict(fwd, **change).values(), None) == rc, change
+    assert lib.muon_expert_product(*dict(fwd, rows=0, xs=None, y=None).values(), None) == 0
+    dgrad = dict(fwd, xs=P, ld_xs=32, y=P, ld_y=64)
+    for change, rc in ((dict(ld_xs=31), -1), (dict(ld_y=63), -1), (dict(dtype=9), -2), (dict(offsets=None), -1)):
+        assert lib.muon_expert_input_grad(*dict(dgrad, **change).values(), None) == rc, change
+    wgrad = dict(dys=P, ld_dys=32, xs=P, ld_xs=64, offsets=P, experts=4, rows=10, inner=64, outer=32, dtype=0, dw=P, ld_dw=64,
+                 stride_dw=64 * 32, dw_dtype=0, accumulate=0, status=None)
+    for change, rc in ((dict(dys=None), -1), (dict(xs=P + 1), -1), (dict(ld_dw=63), -1), (dict(dw=None), -1),
+                       (dict(dw_dtype=1), -2), (dict(accumulate=1), -2), (dict(dtype=1), -2), (dict(stride_dw=0), -1),
+                       (dict(stride_dw=-8), -1), (dict(dw_dtype=2, dw=P + 2), -1)):
+        assert lib.muon_expert_weight_grad(*dict(wgrad, **change).values(), None) == rc, change
+
+
+def _block_group(ptr=P, rows=64, cols=128, count=2, wdt=0, gdt=0, ld=(256, 256, 256)):
+    arrs = [(ctypes.c_void_p * count)(*[ptr + 2 * 128 * i for i in range(count)]) for _ in range(2)]
+    arrs.append((ctypes.c_void_p * count)(*[P + 4 * 128 * i for i in range(count)]))
+    return nsm._BlockGroup(rows, cols, count, wdt, gdt, *ld, *arrs), arrs
+
+
+def test_block_step_refusals(lib):
+    ns, _a = nsm._ns_params((nsm.QUINTIC,) * 5, "standard", 2, 1e-7, "fp16", "fp16")
+    hp = nsm._hparams(0.02, 0.95, 0.1, 0.2, 1, ns)
+    ws = ctypes.c_void_p(1 << 24)
+
+    def call(group, n=1, ws=ws, size=1 << 30, hp=hp):
+        return lib.muon_step_blocks((nsm._BlockGroup * 1)(group), n, ctypes.byref(hp), ws, size, None, None)
+
+    good, keep = _block_group()
+    size = lib.muon_blocks_workspace_size((nsm._BlockGroup * 1)(good), 1, ctypes.byref(hp))
+    assert size == lib.muon_ns_workspace_size(2, 64, 128, ctypes.byref(ns))
+    least = lib.muon_blocks_workspace_min((nsm._BlockGroup * 1)(good), 1, ctypes.byref(hp))
+    assert least == lib.muon_ns_workspace_size(1, 64, 128, ctypes.byref(ns))
+    assert call(good, n=0) == -1 and call(good, ws=None) == -1 and call(good, ws=ctypes.c_void_p((1 << 24) + 8)) == -1
+    assert call(good, size=1024) == -3
+    for kw, rc in ((dict(ptr=P + 1), -1), (dict(rows=0), -1), (dict(cols=-1), -1), (dict(wdt=3), -2), (dict(gdt=-1), -2),
+                   (dict(ld=(127, 256, 256)), -1), (dict(ld=(256, 0, 256)), -1), (dict(ld=(256, 256, 1 << 31)), -1)):
+        bad, keep2 = _block_group(**kw)
+        assert call(bad) == rc, kw
+        assert lib.muon_blocks_workspace_size((nsm._BlockGroup * 1)(bad), 1, ctypes.byref(hp)) == 0
+    # two-byte alignment is enough for 16-bit elements: refused for its size alone
+    odd, keep3 = _block_group(ptr=P + 2)
+    assert call(odd, size=1024) == -3
+    nan = nsm._hparams(0.02, float("nan"), 0.1, 0.2, 1, ns)
+    assert call(good, hp=nan) == -1
+
+
+def test_the_binding_refuses_what_it_cannot_run():
+    x, slot, ids = torch.zeros(4, 8), torch.zeros(4, 2, dtype=torch.int32), torch.zeros(4, 2, dtype=torch.int64)
+    w, offsets = torch.zeros(2, 3, 8), torch.zeros(3, dtype=torch.int32)
+    for call in (lambda: nsm.muon_expert_sort(ids, 4), lambda: nsm.muon_expert_gather(x, slot),
+                 lambda: nsm.muon_expert_combine(x, slot), lambda: nsm.muon_expert_gather_backward(x, slot),
+                 lambda: nsm.muon_expert_combine_backward(x, x, slot), lambda: nsm.muon_expert_product(x, w, offsets),
+                 lambda: nsm.muon_expert_input_grad(x, w, offsets), lambda: nsm.muon_expert_weight_grad(x, x, offsets),
+                 lambda: nsm.muon_step_blocks([x], [x], [x], [(2, 8)]), lambda: nsm.ExpertMuonStep([w], [w]),
+                 lambda: nsm.ExpertMuonStep([], []), lambda: nsm.MuonStep([x], [x], [x], blocks=[(2, 8)])):
+        with pytest.raises(nsm.MuonError):
+            call()
+
+
+class Fake:
+    """A CUDA matrix for the binding's checks alone."""
+
+    def __init__(self, shape, stride=None, dtype=torch.bfloat16, device="cuda:0"):
+        self.shape = torch.Size(shape)
+        self._stride = tuple(stride) if stride else tuple(torch.empty(shape, device="meta").stride())
+        self.dtype, self.device, self.is_cuda = dtype, torch.device(device), True
+
+    def dim(self):
+        return len(self.shape)
+
+    def stride(self, i=None):
+        return self._stride if i is None else self._stride[i]
+
+    def numel(self):
+        return self.shape.numel()
+
+    def element_size(self):
+        return self.dtype.itemsize
+
+    def data_ptr(self):
+        return P
+
+    def is_contiguous(self):
+        return self._stride == tuple(torch.empty(self.shape, device="meta").stride())
+
+
+def test_shapes_types_and_devices_are_checked():
+    bf, i32 = torch.bfloat16, torch.int32
+    x, slot = Fake((4, 8)), Fake((4, 2), dtype=i32)
+    w, offsets = Fake((2, 3, 8)), Fake((3,), dtype=i32)
+    bad = [
+        lambda: nsm.muon_expert_sort(Fake((4, 2), dtype=torch.int16), 4),
+        lambda: nsm.muon_expert_sort(Fake((4,), dtype=i32), 4),
+        lambda: nsm.muon_expert_sort(Fake((4, 2), dtype=i32), 0),
+        lambda: nsm.muon_expert_sort(Fake((4, 2), dtype=i32), 1025),
+        lambda: nsm.muon_expert_sort(Fake((4, 2), (1, 4), dtype=i32), 4),           # columns are not contiguous
+        lambda: nsm.muon_expert_sort(Fake((4, 2), (0, 1), dtype=i32), 4),           # one row, broadcast
+        lambda: nsm.muon_expert_gather(x, Fake((4, 2), dtype=torch.int64)),
+        lambda: nsm.muon_expert_gather(x, Fake((5, 2), dtype=i32)),                 # another number of tokens
+        lambda: nsm.muon_expert_gather(x, Fake((4, 2), dtype=i32, device="cuda:1")),
+        lambda: nsm.muon_expert_gather(Fake((4, 8), dtype=torch.float64), slot),
+        lambda: nsm.muon_expert_gather(Fake((4, 8), (1, 4)), slot),
+        lambda: nsm.muon_expert_gather(Fake((4, 8), (0, 1)), slot),
+        lambda: nsm.muon_expert_gather(x, slot, out=Fake((8, 9))),
+        lambda: nsm.muon_expert_gather(x, slot, out=Fake((8, 8), dtype=torch.float16)),
+        lambda: nsm.muon_expert_combine(x, slot, Fake((4, 3))),
+        lambda: nsm.muon_expert_combine(x, slot, Fake((4, 2), (1, 4))),
+        lambda: nsm.muon_expert_combine(x, slot, Fake((4, 2), device="cuda:1")),
+        lambda: nsm.muon_expert_combine(x, slot, out=Fake((3, 8))),
+        lambda: nsm.muon_expert_combine_backward(Fake((4, 9)), x, slot),
+        lambda: nsm.muon_expert_combine_backward(Fake((4, 8), (0, 1)), x, slot),    # a broadcast gradient
+        lambda: nsm.muon_expert_combine_backward(x, x, slot, out=Fake((5, 8))),
+        lambda: nsm.muon_expert_product(x, Fake((2, 3, 9)), offsets),
+        lambda: nsm.muon_expert_product(x, Fake((3, 3, 8)), offsets),
+        lambda: nsm.muon_expert_product(x, Fake((2, 3, 8), dtype=torch.float16), offsets),
+        lambda: nsm.muon_expert_product(x, w, Fake((3,), dtype=torch.int64)),
+        lambda: nsm.muon_expert_product(x, w, Fake((1,), dtype=i32)),
+        lambda: nsm.muon_expert_product(x, w, offsets, out=Fake((4, 4))),
+        lambda: nsm.muon_expert_product(x, w, offsets, status=Fake((2,), dtype=i32)),
+        lambda: nsm.muon_expert_input_grad(x, w, offsets),
+        lambda: nsm.muon_expert_weight_grad(x, Fake((5, 8)), offsets),
+        lambda: nsm.muon_expert_weight_grad(x, x, offsets, accumulate=True),
+        lambda: nsm.muon_expert_weight_grad(x, x, offsets, out=Fake((2, 8, 9))),
+        lambda: nsm.muon_expert_weight_grad(x, x, offsets, out=Fake((2, 8, 8)), out_dtype=torch.float32),
+        lambda: nsm.muon_expert_weight_grad(x, x, offsets, out_dtype=torch.float64),
+        lambda: nsm.muon_step_blocks([x], [x], [Fake((4, 8), dtype=torch.float32)], [(3, 8)]),
+        lambda: nsm.muon_step_blocks([x], [x], [Fake((4, 8), dtype=torch.float32)], [(2, 8), None]),
+        lambda: nsm.muon_step_blocks([x], [x], [x], [(2, 8)]),
+        lambda: nsm.muon_step_blocks([x], [Fake((8, 4))], [Fake((4, 8), dtype=torch.float32)], [None]),
+        lambda: nsm.muon_step_blocks([x], [Fake((4, 8), (0, 1))], [Fake((4, 8), dtype=torch.float32)], [None]),
+    ]
+    for i, call in enumerate(bad):
+        with pytest.raises(nsm.MuonError):
+            call()
+            raise AssertionError(i)
+
+
+def test_block_groups_name_every_block_once():
+    """Pointers and status order of a strided stack, by hand."""
+    w = Fake((2, 4, 6), (100, 10, 1))
+    m = Fake((2, 4, 6), (24, 6, 1), dtype=torch.float32)
+    groups, n, _keep, order = nsm._build_block_groups([w, w], [w, w], [m, m], [(2, 3), None])
+    assert n == 2 and order == list(range(10))
+    g = groups[0]
+    assert (g.rows, g.cols, g.count, g.ld_w, g.ld_g, g.ld_m) == (2, 3, 8, 10, 10, 6)
+    assert [g.W[i] - P for i in range(8)] == [2 * (100 * e + 10 * i + j) for e in (0, 1) for i in (0, 2) for j in (0, 3)]
+    assert [g.M[i] - P for i in range(8)] == [4 * (24 * e + 6 * i + j) for e in (0, 1) for i in (0, 2) for j in (0, 3)]
+    g = groups[1]
+    assert (g.rows, g.cols, g.count) == (4, 6, 2) and [g.W[i] - P for i in range(2)] == [0, 200]

@@ -1,0 +1,139 @@
+"""The Muon step on the blocks of stacked, fused and strided weights: bit for
+bit muon_step on dense copies of the blocks, and nothing outside them moves."""
+import math
+
+import pytest
+import torch
+
+import newton_schulz_matrix_b200 as nsm
+import oracle
+import synth
+
+pytestmark = pytest.mark.gpu
+TYPES = {"bf16": torch.bfloat16, "fp16": torch.float16, "fp32": torch.float32}
+
+
+def cut(t, block):
+    """Dense copies of a tensor's blocks in the order of its status words."""
+    r, c = block
+    out = []
+    for m in t.reshape(-1, *t.shape[-2:]):
+        out += [m[i:i + r, j:j + c].clone() for i in range(0, m.shape[0], r) for j in range(0, m.shape[1], c)]
+    return out
+
+
+CASES = {
+    # shape, block, view of the storage, W type, G type, hyper-parameters
+    "heads": ((512, 384), (64, 384), None, "bf16", "bf16", {}),
+    "head-columns": ((384, 512), (384, 64), None, "bf16", "bf16", {}),
+    "fused-gate-up": ((3, 1024, 512), (512, 512), None, "bf16", "bf16", {}),
+    "fused-tall": ((2, 600, 512), (600, 256), None, "bf16", "fp32", {}),
+    "stack-of-stacks": ((2, 2, 256, 320), (256, 160), None, "fp16", "fp16", {"compute_dtype": "bf16"}),
+    "strided-rows": ((2, 300, 520), (300, 260), "wide", "bf16", "bf16", {}),
+    "unaligned": ((2, 514, 777), (257, 259), "odd", "bf16", "bf16", {}),
+    "unaligned-fp32": ((300, 603), (300, 201), "odd", "fp32", "bf16", {"compute_dtype": "fp32"}),
+    "fp32-tensor": ((2, 512, 640), (256, 320), "wide", "fp32", "fp32", {"compute_dtype": "fp32"}),
+    "fp32-small": ((3, 64, 130), (32, 65), "odd", "fp32", "fp32", {"compute_dtype": "fp32"}),
+    "gram": ((2, 512, 1536), (256, 768), "wide", "bf16", "bf16", {"mode": "gram_stabilized"}),
+    "no-nesterov": ((320, 640), (320, 320), None, "fp32", "fp16", {"nesterov": False, "weight_decay": 0.0}),
+    "rows-of-one": ((6, 48), (1, 48), None, "bf16", "bf16", {}),
+    "column-of-one": ((40, 3), (40, 1), None, "bf16", "bf16", {}),
+}
+
+
+def make(shape, view, dtype, seed, std):
+    """A tensor of `shape` inside a larger storage of sevens, and that storage."""
+    pad = {None: 0, "wide": 24, "odd": 3}[view]
+    store = torch.full(shape[:-2] + (shape[-2] + (2 if pad else 0), shape[-1] + pad), 7.0, dtype=dtype, device="cuda")
+    first = 1 if view == "odd" else 0
+    t = store[..., :shape[-2], first:first + shape[-1]]
+    n = math.prod(shape)
+    t.copy_(synth.gaussian(1, n, seed, "cuda", std=std).view(shape).to(dtype))
+    return t, store
+
+
+@pytest.mark.parametrize("name", sorted(CASES))
+def test_blocks_step_as_dense_copies_do(name):
+    shape, block, view, wdt, gdt, hp = CASES[name]
+    (w, ws), (g, gs), (m, ms) = (make(shape, view, TYPES[wdt], 1, 0.05), make(shape, view, TYPES[gdt], 2, 1.0),
+                                 make(shape, view, torch.float32, 3, 0.2))
+    wd, gd, md = (cut(t, block) for t in (w, g, m))
+    before = [t.clone() for t in (ws, gs, ms)]
+    nsm.muon_step(wd, gd, md, **hp)
+    status = torch.full((len(wd),), -1, dtype=torch.int32, device="cuda")
+    nsm.muon_step_blocks([w], [g], [m], [block], status=status, **hp)
+    assert status.tolist() == [0] * len(wd)
+    for got, want in zip(cut(w, block) + cut(m, block), wd + md):
+        assert torch.equal(got, want)
+    # the storage around the blocks, and G, are as they were
+    for t, view_, was in ((ws, w, before[0]), (ms, m, before[2])):
+        view_.copy_(torch.zeros_like(view_))
+        outside = t.clone()
+        t.copy_(was)
+        view_.copy_(torch.zeros_like(view_))
+        assert torch.equal(outside, t)
+    assert torch.equal(gs, before[1])
+
+
+def test_parameters_of_several_kinds_in_one_call():
+    """Heads, their transposes and whole matrices orient to common shapes and share batches; each gets its own result and status."""
+    specs = [((4, 256, 640), (256, 320)), ((640, 512), (320, 256)), ((2, 320, 256), None), ((256, 320), None)]
+    ws, gs, ms = [], [], []
+    for i, (shape, _) in enumerate(specs):
+        ws.append(make(shape, None, torch.bfloat16, 10 + i, 0.05)[0])
+        gs.append(make(shape, None, torch.bfloat16, 20 + i, 1.0)[0])
+        ms.append(make(shape, None, torch.float32, 30 + i, 0.2)[0])
+    gs[1][400, 300] = float("nan")  # its block: rows 320.., columns 256..: the last of four
+    blocks = [b for _, b in specs]
+    dense = [[c for t, (s, b) in zip(ts, specs) for c in cut(t, b or s[-2:])] for ts in (ws, gs, ms)]
+    want = torch.full((len(dense[0]),), -1, dtype=torch.int32, device="cuda")
+    nsm.muon_step(*dense, status=want)
+    status = torch.full_like(want, -1)
+    nsm.muon_step_blocks(ws, gs, ms, blocks, status=status)
+    assert torch.equal(status, want) and status.tolist() == [0] * 11 + [1] + [0] * 3
+    got = [c for ts in (ws, ms) for t, (s, b) in zip(ts, specs) for c in cut(t, b or s[-2:])]
+    for a, b in zip(got, dense[0] + dense[2]):
+        assert torch.equal(a.view(torch.int16 if a.element_size() == 2 else torch.int32),
+                           b.view(torch.int16 if b.element_size() == 2 else torch.int32))
+
+
+def test_blocks_against_the_oracle():
+    q5 = [oracle.QUINTIC] * 5
+    w, g, m = (make((2, 256, 384), None, torch.float32, 40 + i, s)[0] for i, s in enumerate((0.05, 1.0, 0.2)))
+    old = [t.double().cpu().numpy() for t in (w, g, m)]
+    nsm.muon_step_blocks([w], [g], [m], [(128, 384)], compute_dtype="fp32")
+    for e in range(2):
+        for i in (0, 128):
+            ref, mref, o = oracle.muon_step(*[t[e, i:i + 128] for t in old], lr=0.02, momentum=0.95, nesterov=True,
+                                            weight_decay=0.1, scale_coef=0.2, eps=1e-7, coeffs=q5)
+            step = torch.from_numpy(o).norm() * 0.02 * 0.2 * math.sqrt(384)
+            # 1e-4 of the step (the fp32 bar) and half an fp32 step of the weights, three roundings
+            assert (w[e, i:i + 128].double().cpu() - torch.from_numpy(ref)).norm() <= 1e-4 * step + 3 * 2.0 ** -24 * torch.from_numpy(ref).norm()
+            assert (m[e, i:i + 128].double().cpu() - torch.from_numpy(mref)).norm() <= 3 * 2.0 ** -24 * torch.from_numpy(mref).norm()
+
+
+def test_a_prepared_block_step_captures_and_uses_small_workspaces():
+    shape, block = (4, 512, 512), (256, 512)
+    w, g, m = (make(shape, None, dt, 50 + i, s)[0] for i, (dt, s) in enumerate(
+        ((torch.bfloat16, 0.05), (torch.bfloat16, 1.0), (torch.float32, 0.2))))
+    start = [w.clone(), m.clone()]
+    nsm.muon_step_blocks([w], [g], [m], [block])
+    nsm.muon_step_blocks([w], [g], [m], [block])
+    want = [w.clone(), m.clone()]
+    lo, hi = (f([w], [g], [m], [block]) for f in (nsm.muon_blocks_workspace_min, nsm.muon_blocks_workspace_size))
+    assert lo < hi
+    w.copy_(start[0]), m.copy_(start[1])
+    step = nsm.MuonStep([w], [g], [m], blocks=[block], workspace_bytes=3 * lo)
+    graph = step.capture()  # one eager step
+    graph.replay()
+    assert step.status.tolist() == [0] * 8
+    for a, b in zip((w, m), want):
+        assert torch.equal(a, b)
+    w.copy_(start[0]), m.copy_(start[1])
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for _ in range(2):
+        nsm.muon_step_blocks([w], [g], [m], [block], stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    for a, b in zip((w, m), want):
+        assert torch.equal(a, b)

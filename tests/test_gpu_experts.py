@@ -1,0 +1,460 @@
+"""The expert-layer operators against plain 64-bit versions: routing (sort,
+gather, combine and gradients), the experts' products and their gradients, and
+a whole layer's training step into the Muon step."""
+import pytest
+import torch
+
+import newton_schulz_matrix_b200 as nsm
+import oracle
+from expert_util import U_NEAREST, U_TRUNCATED, close, f64, rows_ref, segments, sort_ref
+
+pytestmark = pytest.mark.gpu
+BF, HF, SF = torch.bfloat16, torch.float16, torch.float32
+
+
+def gen(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def randn(g, *shape, dtype=SF):
+    return torch.randn(*shape, generator=g, device="cuda").to(dtype)
+
+
+def routing(seed, tokens, topk, experts, dropped=0.0, dtype=torch.int64):
+    g = gen(seed)
+    ids = torch.rand(tokens, experts, generator=g, device="cuda").topk(topk, dim=1).indices
+    keep = torch.rand(tokens, topk, generator=g, device="cuda") >= dropped
+    return torch.where(keep, ids, -1).to(dtype)
+
+
+def pitched(t, pad):
+    """The same matrix with `pad` elements between its rows, and that storage."""
+    store = torch.full((t.shape[0], t.shape[1] + pad), float("nan"), dtype=t.dtype, device=t.device)
+    view = store[:, :t.shape[1]]
+    view.copy_(t)
+    return view
+
+
+# ---------------------------------------------------------------- sort
+@pytest.mark.parametrize("dtype", [torch.int32, torch.int64])
+@pytest.mark.parametrize("tokens,topk,experts", [
+    (1, 1, 1), (1, 8, 8), (3, 2, 1024), (32, 8, 216), (33, 3, 7), (1000, 8, 64), (1024, 8, 1023), (1025, 8, 64),
+    (4097, 2, 1024), (20011, 3, 13), (70000, 8, 256)])
+def test_sort_is_the_stable_order(tokens, topk, experts, dtype):
+    ids = routing(1, tokens, min(topk, experts), experts, 0.1, dtype)
+    got = nsm.muon_expert_sort(ids, experts)
+    for g, r in zip(got, sort_ref(ids, experts)):
+        assert g.dtype == torch.int32 and torch.equal(g.cpu(), r)
+
+
+def test_sort_of_extreme_ids():
+    """Ids outside the range (negative, beyond int32, the first one past the end) go to no expert; one expert may take all."""
+    ids = torch.tensor([[0, 4], [5, -1], [2 ** 40, -2 ** 40], [2 ** 32, 2 ** 32 + 3], [4, 4]], device="cuda")
+    for g, r in zip(nsm.muon_expert_sort(ids, 5), sort_ref(ids, 5)):
+        assert torch.equal(g.cpu(), r)
+    for tokens in (7, 30000):
+        one = torch.full((tokens, 2), 3, device="cuda")
+        none = torch.full((tokens, 2), -1, device="cuda", dtype=torch.int32)
+        for ids in (one, none):
+            for g, r in zip(nsm.muon_expert_sort(ids, 9), sort_ref(ids, 9)):
+                assert torch.equal(g.cpu(), r)
+
+
+def test_sort_of_no_token_and_of_pitched_ids():
+    offsets, slot, source = nsm.muon_expert_sort(torch.empty(0, 4, dtype=torch.int64, device="cuda"), 6)
+    assert offsets.tolist() == [0] * 7 and slot.shape == (0, 4) and source.numel() == 0
+    wide = routing(2, 9000, 8, 32)
+    for ids in (wide[:, 2:5], wide[::3, :4]):
+        for g, r in zip(nsm.muon_expert_sort(ids, 32), sort_ref(ids, 32)):
+            assert torch.equal(g.cpu(), r)
+
+
+# ---------------------------------------------------------------- gather and combine
+ROUTES = [  # tokens, topk, experts, cols, dropped, pad
+    (1, 1, 1, 1, 0.0, 0), (1, 8, 16, 7168, 0.0, 0), (5, 3, 4, 17, 0.3, 0), (64, 8, 216, 2048, 0.0, 0),
+    (257, 2, 8, 1001, 0.5, 0), (130, 6, 64, 96, 0.2, 8), (33, 11, 12, 130, 0.4, 2), (40, 4, 8, 264, 0.1, 3),
+    (9, 2, 3, 8, 1.0, 0)]
+
+
+@pytest.mark.parametrize("dtype", [BF, HF, SF])
+@pytest.mark.parametrize("tokens,topk,experts,cols,dropped,pad", ROUTES)
+def test_gather_and_its_gradient(tokens, topk, experts, cols, dropped, pad, dtype):
+    g = gen(3)
+    offsets, slot, source = nsm.muon_expert_sort(routing(4, tokens, topk, experts, dropped), experts)
+    x, dxs = pitched(randn(g, tokens, cols, dtype=dtype), pad), pitched(randn(g, tokens * topk, cols, dtype=dtype), pad)
+    used = int(offsets[-1])
+    dxs[used:] = float("nan")  # rows that no assignment names
+    out = pitched(torch.full((tokens * topk, cols), 7.0, dtype=dtype, device="cuda"), pad)
+    assert nsm.muon_expert_gather(x, slot, out=out) is out
+    token = source[:used].long() // topk
+    assert torch.equal(out[:used], x[token]) and bool((out[used:] == 7).all())
+    dx = nsm.muon_expert_gather_backward(dxs, slot)
+    rows, _ = rows_ref(torch.where(torch.arange(tokens * topk, device="cuda")[:, None] < used, dxs, 0), slot)
+    close(dx, rows.sum(1), topk, rows.abs().sum(1), U_NEAREST)
+
+
+@pytest.mark.parametrize("wdtype", [SF, BF])
+@pytest.mark.parametrize("dtype", [BF, HF, SF])
+@pytest.mark.parametrize("tokens,topk,experts,cols,dropped,pad", ROUTES)
+def test_combine_and_its_gradients(tokens, topk, experts, cols, dropped, pad, dtype, wdtype):
+    g = gen(5)
+    offsets, slot, _ = nsm.muon_expert_sort(routing(6, tokens, topk, experts, dropped), experts)
+    used = int(offsets[-1])
+    ys, dy = pitched(randn(g, tokens * topk, cols, dtype=dtype), pad), pitched(randn(g, tokens, cols, dtype=dtype), pad)
+    ys[used:] = float("inf")
+    w = randn(g, tokens, topk, dtype=wdtype)
+    w = torch.where(slot >= 0, w, float("nan"))  # the weight of a dropped assignment does not matter
+    y = nsm.muon_expert_combine(ys, slot, w)
+    rows, on = rows_ref(ys[:used], slot)
+    w64 = torch.where(on, f64(w), 0.0)
+    close(y, (w64[..., None] * rows).sum(1), topk, (w64[..., None] * rows).abs().sum(1), U_NEAREST)
+    out = pitched(torch.full((tokens * topk, cols), 7.0, dtype=dtype, device="cuda"), pad)
+    dys, dw = nsm.muon_expert_combine_backward(dy, ys, slot, w, out=out)
+    assert dys is out and bool((dys[used:] == 7).all()) and dw.dtype == wdtype
+    dy64 = f64(dy)[:, None, :]
+    want = (w64[..., None] * dy64)
+    picked, _ = rows_ref(dys, slot)
+    close(dys[:used], want[on].new_zeros(used, cols).index_copy_(0, slot.cpu()[on].long(), want[on]), 1,
+          want[on].new_zeros(used, cols).index_copy_(0, slot.cpu()[on].long(), want[on].abs()), U_NEAREST)
+    close(dw, (rows * dy64).sum(2), cols, (rows * dy64).abs().sum(2), U_NEAREST)
+
+
+def test_combine_without_weights_and_inf_in_a_taken_row():
+    slot = torch.tensor([[0, -1], [1, 2]], dtype=torch.int32, device="cuda")
+    ys = torch.tensor([[1.0, float("inf")], [2.0, 3.0], [4.0, float("nan")]], device="cuda")
+    y = nsm.muon_expert_combine(ys, slot)
+    assert y[0].tolist() == [1.0, float("inf")] and y[1, 0] == 6.0 and bool(y[1, 1].isnan())
+    dys, dw = nsm.muon_expert_combine_backward(torch.ones(2, 2, device="cuda"), ys, slot)
+    assert dw is None and dys.tolist() == [[1.0, 1.0]] * 3
+
+
+def test_slots_outside_the_rows_are_skipped():
+    """A slot beyond the sorted matrix (an output cut to a capacity) touches nothing."""
+    g = gen(7)
+    x = randn(g, 6, 40, dtype=BF)
+    slot = torch.tensor([[0], [3], [4], [5], [2 ** 31 - 1], [-2 ** 31]], dtype=torch.int32, device="cuda")
+    store = torch.full((6, 40), 7.0, dtype=BF, device="cuda")
+    nsm.muon_expert_gather(x, slot, out=store[:4])
+    assert torch.equal(store[0], x[0]) and torch.equal(store[3], x[1])
+    assert bool((store[1:3] == 7).all()) and bool((store[4:] == 7).all())
+    y = nsm.muon_expert_combine(store[:4], slot)
+    assert torch.equal(y[:2], x[:2]) and not y[2:].any()
+    dys, dw = nsm.muon_expert_combine_backward(x, store[:4], slot, torch.ones(6, 1, device="cuda"))
+    assert dys.shape == (4, 40) and not dw[2:].any()
+
+
+# ---------------------------------------------------------------- products
+def offsets_of(counts, first=0):
+    return torch.tensor([first] + counts, dtype=torch.int32).cumsum(0).to(torch.int32).cuda()
+
+
+PRODUCTS = [  # counts, inner, outer
+    ([1], 64, 64), ([0, 0, 3], 16, 8), ([5, 0, 17, 1], 72, 40), ([130, 64, 0, 255], 256, 264), ([256, 257, 511], 128, 512),
+    ([33] * 20, 320, 136), ([700, 2, 0, 90], 1000, 520), ([15, 16, 17, 31, 32, 33, 47, 48, 49, 63, 64, 65], 192, 256),
+    ([1024], 512, 768)]
+
+
+def product_case(seed, counts, inner, outer, dtype, tail=3, pad=0):
+    g = gen(seed)
+    rows = sum(counts) + tail
+    xs, dys = pitched(randn(g, rows, inner, dtype=dtype), pad), pitched(randn(g, rows, outer, dtype=dtype), pad)
+    # what lies behind the last expert's rows reaches no result
+    xs[sum(counts):] = float("nan")
+    dys[sum(counts):] = float("inf")
+    return offsets_of(counts), xs, dys, randn(g, len(counts), outer, inner, dtype=dtype)
+
+
+def check_products(offsets, xs, dys, w, u, dw_dtype=None):
+    rows, inner, outer, dtype = xs.shape[0], xs.shape[1], dys.shape[1], xs.dtype
+    y = torch.full((rows, outer), 7.0, dtype=dtype, device="cuda")
+    dx = torch.full((rows, inner), 7.0, dtype=dtype, device="cuda")
+    status = torch.full((1,), -1, dtype=torch.int32, device="cuda")
+    nsm.muon_expert_product(xs, w, offsets, out=y, status=status)
+    assert int(status) == 0
+    nsm.muon_expert_input_grad(dys, w, offsets, out=dx, status=status)
+    assert int(status) == 0
+    dw = nsm.muon_expert_weight_grad(dys, xs, offsets, out_dtype=dw_dtype, status=status)
+    assert int(status) == 0
+    owned = torch.zeros(rows, dtype=torch.bool)
+    for e, (lo, hi) in enumerate(segments(offsets, rows)):
+        owned[lo:hi] = True
+        x, d, m = f64(xs[lo:hi]), f64(dys[lo:hi]), f64(w[e])
+        close(y[lo:hi], x @ m.T, inner, x.abs() @ m.abs().T, u, f"y of expert {e}")
+        close(dx[lo:hi], d @ m, outer, d.abs() @ m.abs(), u, f"dx of expert {e}")
+        close(dw[e], d.T @ x, hi - lo, d.abs().T @ x.abs(), u, f"dw of expert {e}")
+    assert bool((y[~owned] == 7).all()) and bool((dx[~owned] == 7).all())
+
+
+@pytest.mark.parametrize("dtype", [BF, HF, SF])
+@pytest.mark.parametrize("counts,inner,outer", PRODUCTS)
+def test_products_and_gradients(counts, inner, outer, dtype):
+    check_products(*product_case(11, counts, inner, outer, dtype), U_NEAREST if dtype == SF else U_TRUNCATED,
+                   SF if counts[0] % 2 else None)
+
+
+@pytest.mark.parametrize("dtype", [BF, SF])
+@pytest.mark.parametrize("inner,outer,pad", [(33, 130, 0), (72, 41, 1), (64, 64, 3), (264, 1, 0), (1, 136, 8)])
+def test_products_of_odd_widths_and_pitches(inner, outer, pad, dtype):
+    check_products(*product_case(12, [7, 0, 66, 3], inner, outer, dtype, pad=pad),
+                   U_NEAREST if dtype == SF else U_TRUNCATED)
+
+
+@pytest.mark.parametrize("dtype", [BF, SF])
+def test_products_of_strided_weights(dtype):
+    """Weights that are part of a fused stack: every second half of the rows, a slice of the columns; dW written into one."""
+    g = gen(13)
+    counts = [40, 0, 300]
+    offsets, xs, dys, _ = product_case(14, counts, 128, 96, dtype)
+    fused = randn(g, 3, 2 * 96, 128 + 64, dtype=dtype)
+    w = fused[:, 96:, 64:]
+    check_products(offsets, xs, dys, w, U_NEAREST if dtype == SF else U_TRUNCATED)
+    assert torch.equal(nsm.muon_expert_product(xs, w, offsets)[:340], nsm.muon_expert_product(xs, w.contiguous(), offsets)[:340])
+    out = torch.full((3, 2 * 96, 128 + 64), 7.0, dtype=dtype, device="cuda")
+    nsm.muon_expert_weight_grad(dys, xs, offsets, out=out[:, 96:, 64:])
+    assert torch.equal(out[:, 96:, 64:], nsm.muon_expert_weight_grad(dys, xs, offsets))
+    assert bool((out[:, :96] == 7).all()) and bool((out[:, :, :64] == 7).all())
+
+
+@pytest.mark.parametrize("dtype", [BF, HF, SF])
+def test_nan_stays_with_its_expert(dtype):
+    """Inf and NaN in one expert's rows reach no other expert's results, whatever tile they share."""
+    counts = [21, 9, 34, 100, 3]
+    offsets, xs, dys, w = product_case(15, counts, 128, 64, dtype, tail=0)
+    clean = [f(a, b, offsets) for f, a, b in ((nsm.muon_expert_product, xs, w), (nsm.muon_expert_input_grad, dys, w),
+                                              (nsm.muon_expert_weight_grad, dys, xs))]
+    xs[21:30], dys[21:30] = float("nan"), float("inf")
+    dirty = [f(a, b, offsets) for f, a, b in ((nsm.muon_expert_product, xs, w), (nsm.muon_expert_input_grad, dys, w),
+                                              (nsm.muon_expert_weight_grad, dys, xs))]
+    rest = torch.cat([torch.arange(21), torch.arange(30, 167)]).cuda()
+    for a, b in zip(clean[:2], dirty[:2]):
+        assert torch.equal(a[rest], b[rest])
+    assert torch.equal(clean[2][[0, 2, 3, 4]], dirty[2][[0, 2, 3, 4]]) and not dirty[2][1].isfinite().any()
+
+
+@pytest.mark.parametrize("dtype", [BF, SF])
+@pytest.mark.parametrize("ends", [[5, 40, 40, 90], [-4, 20, 10, 2 ** 31 - 1], [50, 20, 60, 200], [0, 0, 0, 0], [100, 90, 80, 95]])
+def test_offsets_are_clamped_to_the_rows(ends, dtype):
+    """Offsets that start late, run backwards or past the end name the clamped rows and nothing else."""
+    g = gen(16)
+    xs, dys, w = randn(g, 80, 64, dtype=dtype), randn(g, 80, 72, dtype=dtype), randn(g, 3, 72, 64, dtype=dtype)
+    offsets = torch.tensor(ends, dtype=torch.int32, device="cuda")
+    spans = segments(offsets, 80)
+    y = torch.full((81, 72), 7.0, dtype=dtype, device="cuda")
+    nsm.muon_expert_product(xs, w, offsets, out=y[:80])
+    dw = nsm.muon_expert_weight_grad(dys, xs, offsets)
+    u = U_NEAREST if dtype == SF else U_TRUNCATED
+    owners = [[e for e, (lo, hi) in enumerate(spans) if lo <= p < hi] for p in range(81)]
+    for p, own in enumerate(owners):
+        if not own:
+            assert bool((y[p] == 7).all())
+        elif len(own) == 1:
+            a, m = f64(xs[p]), f64(w[own[0]])
+            close(y[p], m @ a, 64, m.abs() @ a.abs(), u)
+    for e, (lo, hi) in enumerate(spans):
+        d, x = f64(dys[lo:hi]), f64(xs[lo:hi])
+        close(dw[e], d.T @ x, hi - lo, d.abs().T @ x.abs(), u)
+
+
+@pytest.mark.parametrize("dtype", [BF, HF, SF])
+def test_weight_gradients_accumulate(dtype):
+    offsets, xs, dys, _ = product_case(17, [300, 0, 41], 136, 264, dtype)
+    base = randn(gen(18), 3, 264, 136)
+    out = base.clone()
+    one = nsm.muon_expert_weight_grad(dys, xs, offsets, out_dtype=SF)
+    assert nsm.muon_expert_weight_grad(dys, xs, offsets, out=out, accumulate=True) is out
+    for e, (lo, hi) in enumerate(segments(offsets, xs.shape[0])):
+        d, x = f64(dys[lo:hi]), f64(xs[lo:hi])
+        u = U_NEAREST if dtype == SF else U_TRUNCATED
+        close(out[e], f64(base[e]) + d.T @ x, hi - lo + 1, f64(base[e]).abs() + d.abs().T @ x.abs(), u)
+    assert torch.equal(out[1], base[1]) and not one[1].any()
+
+
+@pytest.mark.parametrize("rows,experts", [(1, 64), (8, 64), (200, 64), (3000, 300)])
+def test_products_of_many_experts_with_few_rows(rows, experts):
+    g = gen(19)
+    to = torch.randint(0, experts, (rows,), generator=g, device="cuda").sort().values
+    counts = torch.bincount(to, minlength=experts).tolist()
+    check_products(*product_case(20, counts, 256, 128, BF, tail=0), U_TRUNCATED)
+
+
+def test_products_repeat_bit_for_bit_and_on_another_stream():
+    offsets, xs, dys, w = product_case(21, [70, 513, 1, 260], 512, 320, HF)
+    used = int(offsets[-1])
+    calls = [lambda **k: nsm.muon_expert_product(xs, w, offsets, **k)[:used],
+             lambda **k: nsm.muon_expert_input_grad(dys, w, offsets, **k)[:used],
+             lambda **k: nsm.muon_expert_weight_grad(dys, xs, offsets, out_dtype=SF, **k)]
+    side = torch.cuda.Stream()
+    for call in calls:
+        first = call()
+        assert torch.equal(first, call())
+        side.wait_stream(torch.cuda.current_stream())
+        other = call(stream=side)
+        torch.cuda.current_stream().wait_stream(side)
+        assert torch.equal(first, other)
+
+
+# ---------------------------------------------------------------- together
+def layer(x, ids, probs, w1, w2, blocks_dtype=BF):
+    """Forward and backward of a two-product expert layer with relu-squared between, and all that it leaves."""
+    experts = w1.shape[0]
+    offsets, slot, _ = nsm.muon_expert_sort(ids, experts)
+    xs = torch.zeros(ids.numel(), x.shape[1], dtype=x.dtype, device="cuda")
+    nsm.muon_expert_gather(x, slot, out=xs)
+    h = nsm.muon_expert_product(xs, w1, offsets, out=torch.zeros(ids.numel(), w1.shape[1], dtype=x.dtype, device="cuda"))
+    a = torch.relu(h.float()).square().to(x.dtype)
+    o = nsm.muon_expert_product(a, w2, offsets, out=torch.zeros(ids.numel(), w2.shape[1], dtype=x.dtype, device="cuda"))
+    y = nsm.muon_expert_combine(o, slot, probs)
+
+    def backward(dy):
+        do, dprobs = nsm.muon_expert_combine_backward(dy, o, slot, probs, out=torch.zeros_like(o))
+        dw2 = nsm.muon_expert_weight_grad(do, a, offsets)
+        da = nsm.muon_expert_input_grad(do, w2, offsets, out=torch.zeros_like(a))
+        dh = (da.float() * 2 * torch.relu(h.float())).to(x.dtype)
+        dw1 = nsm.muon_expert_weight_grad(dh, xs, offsets)
+        dxs = nsm.muon_expert_input_grad(dh, w1, offsets, out=torch.zeros_like(xs))
+        return nsm.muon_expert_gather_backward(dxs, slot), dprobs, dw1, dw2, (dh, xs, offsets), (do, a, offsets)
+
+    return y, backward
+
+
+def layer_ref(x, ids, probs, w1, w2):
+    """The same layer in 64 bits, one token and one assignment at a time."""
+    y = []
+    for t in range(x.shape[0]):
+        row = torch.zeros(w2.shape[1], dtype=torch.float64)
+        for j in range(ids.shape[1]):
+            e = int(ids[t, j])
+            if 0 <= e < w1.shape[0]:
+                row = row + probs[t, j] * (w2[e] @ torch.relu(w1[e] @ x[t]).square())
+        y.append(row)
+    return torch.stack(y)
+
+
+@pytest.mark.parametrize("dtype", [SF, BF])
+def test_a_layer_and_its_gradients(dtype):
+    """Against the 64-bit layer, its autograd and its differences.  In fp32 the
+    chain of four sums is within 1e-5 of the largest value (terms of at most
+    136 products each, 136 * 2^-24 = 8e-6); in bf16 every stored matrix adds
+    half a step of 2^-8 = 4e-3, eight stores on the longest path: 3.2e-2."""
+    g = gen(30)
+    tokens, topk, experts, width, hidden = 50, 3, 5, 64, 136
+    ids = routing(31, tokens, topk, experts, 0.2)
+    x, w1, w2 = (randn(g, tokens, width, dtype=dtype), (randn(g, experts, hidden, width) / 8).to(dtype),
+                 (randn(g, experts, width, hidden) / 12).to(dtype))
+    probs, dy = torch.rand(tokens, topk, generator=g, device="cuda"), randn(g, tokens, width, dtype=dtype)
+    y, backward = layer(x, ids, probs, w1, w2)
+    grads = backward(dy)[:4]
+    leaves = [f64(t).requires_grad_() for t in (x, probs, w1, w2)]
+    ref = layer_ref(leaves[0], ids.cpu(), *leaves[1:])
+    want = torch.autograd.grad((ref * f64(dy)).sum(), leaves)
+    tol = 1e-5 if dtype == SF else 3.2e-2
+    for got, r in zip((y,) + grads, (ref.detach(),) + want):
+        assert (f64(got) - r).norm() <= tol * r.norm(), float((f64(got) - r).norm() / r.norm())
+    if dtype == SF:
+        # the formula's gradient against central differences of the layer itself
+        h = 2.0 ** -6
+        for i, leaf in enumerate(leaves):
+            step = torch.zeros_like(leaf)
+            at = tuple(int(v) for v in torch.nonzero(want[i].abs() == want[i].abs().max())[0])
+            step[at] = h
+            up, down = ([(v + s * step).detach() if k == i else v.detach() for k, v in enumerate(leaves)] for s in (1, -1))
+            slope = ((layer_ref(up[0], ids.cpu(), *up[1:]) - layer_ref(down[0], ids.cpu(), *down[1:])) * f64(dy)).sum() / (2 * h)
+            # the layer is piecewise polynomial of degree 2 in each leaf: the central difference is exact off its kinks
+            assert abs(float(grads[i].cpu()[at]) - float(slope)) <= 1e-2 * abs(float(slope))
+
+
+def test_a_training_step_of_a_layer():
+    """Route, multiply, differentiate and step: ExpertMuonStep in slices is the weight
+    gradients followed by the block step, bit for bit, and the oracle's step on
+    each expert's halves."""
+    g = gen(32)
+    tokens, topk, experts, width, hidden = 300, 2, 6, 128, 96
+    ids = routing(33, tokens, topk, experts, 0.1)
+    ids[ids == 4] = -1  # an expert without tokens: its momentum decays, its weights decay
+    x = randn(g, tokens, width, dtype=BF)
+    w1, w2 = (randn(g, experts, 2 * hidden, width) / 8).to(BF), (randn(g, experts, width, 2 * hidden) / 12).to(BF)
+    moms = [randn(g, *w.shape) * 0.01 for w in (w1, w2)]
+    moms[0][4], moms[1][4] = 0, 0
+    probs = torch.rand(tokens, topk, generator=g, device="cuda")
+    _, backward = layer(x, ids, probs, w1, w2)
+    *_, dw1, dw2, f1, f2 = backward(randn(g, tokens, width, dtype=BF))
+    blocks = [(hidden, width), None]
+    pa, ma = [w1.clone(), w2.clone()], [m.clone() for m in moms]
+    status = torch.full((3 * experts,), -1, dtype=torch.int32, device="cuda")
+    nsm.muon_step_blocks(pa, [dw1, dw2], ma, blocks, status=status)
+    assert status.tolist() == [0] * (3 * experts)
+    for slice_bytes in (1, 2 * hidden * width * 2 * 4, 1 << 30):
+        pb, mb = [w1.clone(), w2.clone()], [m.clone() for m in moms]
+        step = nsm.ExpertMuonStep(pb, mb, blocks=blocks, slice_bytes=slice_bytes)
+        step([f1, f2])
+        assert step.status.tolist() == [0] * (3 * experts)
+        for a, b in zip(pa + ma, pb + mb):
+            assert torch.equal(a, b)
+    q5 = [oracle.QUINTIC] * 5
+    for w, dw, m, new, (r, c) in ((w1, dw1, moms[0], pa[0], blocks[0]), (w2, dw2, moms[1], pa[1], (width, 2 * hidden))):
+        for e in range(experts):
+            for i in range(0, w.shape[1], r):
+                args = [f64(t[e, i:i + r]).numpy() for t in (w, dw, m)]
+                ref, _, o = oracle.muon_step(*args, lr=0.02, momentum=0.95, nesterov=True, weight_decay=0.1,
+                                             scale_coef=0.2, eps=1e-7, coeffs=q5)
+                err = (f64(new[e, i:i + r]) - torch.from_numpy(ref)).norm()
+                # 2e-2 of the step (the 16-bit chain's bar) and half a bf16 step of the weights
+                step_norm = 0.02 * 0.2 * max(r, c) ** 0.5 * torch.from_numpy(o).norm()
+                assert err <= 2e-2 * step_norm + 2.0 ** -8 * torch.from_numpy(ref).norm()
+
+
+def test_a_captured_layer_replays():
+    """The whole run in one CUDA graph, replayed on other tokens and routes."""
+    g = gen(34)
+    tokens, topk, experts, width, hidden = 200, 2, 4, 64, 128
+    x, ids = randn(g, tokens, width, dtype=BF), routing(35, tokens, topk, experts)
+    probs, dy = torch.rand(tokens, topk, generator=g, device="cuda"), randn(g, tokens, width, dtype=BF)
+    w1, w2 = (randn(g, experts, hidden, width) / 8).to(BF), (randn(g, experts, width, hidden) / 12).to(BF)
+    moms = [torch.zeros(*w.shape, device="cuda") for w in (w1, w2)]
+    step = nsm.ExpertMuonStep([w1, w2], moms, slice_bytes=hidden * width * 4)
+
+    def run():
+        y, backward = layer(x, ids, probs, w1, w2)
+        out = backward(dy)
+        step([out[4], out[5]])
+        return (y,) + out[:4]
+
+    start = [t.clone() for t in [w1, w2] + moms]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        run()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured = run()
+    for seed in (36, 37):
+        g = gen(seed)
+        x.copy_(randn(g, tokens, width, dtype=BF))
+        ids.copy_(routing(seed, tokens, topk, experts, 0.3))
+        results = []
+        for replay in (True, False):
+            for t, s in zip([w1, w2] + moms, start):
+                t.copy_(s)
+            if replay:
+                graph.replay()
+                out = captured
+            else:
+                out = run()
+            results.append([t.clone() for t in list(out) + [w1, w2] + moms])
+        for a, b in zip(*results):
+            assert torch.equal(a, b)
+
+
+def test_expert_launches_are_profiled():
+    offsets, xs, dys, w = product_case(38, [100, 28], 64, 64, BF)
+    nsm.muon_profile_begin()
+    offs, slot, _ = nsm.muon_expert_sort(routing(39, 64, 2, 4), 4)
+    rows = nsm.muon_expert_gather(randn(gen(40), 64, 32, dtype=BF), slot)
+    nsm.muon_expert_combine_backward(nsm.muon_expert_combine(rows, slot), rows, slot)
+    nsm.muon_expert_product(xs, w, offsets)
+    nsm.muon_expert_weight_grad(dys.float(), xs.float(), offsets)
+    prof = {r["kernel"]: r for r in nsm.muon_profile_end()}
+    for name in ("expert_sort", "expert_gather", "expert_combine", "expert_combine_backward"):
+        assert prof[name]["launches"] == 1 and prof[name]["ms"] > 0, name
+    assert sum(r["launches"] for name, r in prof.items() if name.startswith("expert_product")) == 2
