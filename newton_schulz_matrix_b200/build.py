@@ -18,7 +18,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libmuon.so")
-SOURCES = ["api.cu", "elementwise.cu", "expert_api.cu", "expert_route.cu", "expert_simt.cu", "gemm_chain.cu", "gemm_simt.cu",
+SOURCES = ["api.cu", "elementwise.cu", "expert_api.cu", "expert_route.cu", "expert_simt.cu", "expert_tc.cu",
+           "gemm_chain.cu", "gemm_simt.cu",
            "gemm_tc.cu", "gemm_tc2.cu", "gemm_tf32.cu", "noalloc.cu"]
 HEADERS = ["common.cuh", "expert.h", "internal.h", "profile.h", "tc_common.cuh"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]

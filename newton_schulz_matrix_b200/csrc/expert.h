@@ -53,6 +53,8 @@ struct ExpertDesc {
   int d_dtype; int accumulate;               // kWeightGrad only
   int* status;                 // device word for MUON_STATUS_TIMEOUT, or null
 };
+bool expert_tc_ok(const ExpertDesc& g);   // whether expert_tc takes it: 16-bit operands that TMA can address
+int expert_tc(const ExpertDesc& g, cudaStream_t s);     // tensor cores (expert_tc.cu)
 int expert_simt(const ExpertDesc& g, cudaStream_t s);   // any type, alignment and pitch (expert_simt.cu)
 
 }  // namespace muon

@@ -62,8 +62,9 @@ int run_product(const ExpertDesc& g, cudaStream_t s) {
   const double es = dtype_size(g.dtype);
   const double bytes = (double)g.rows * (g.inner + g.outer) * es +
                        (double)g.experts * g.inner * g.outer * (g.kind == kWeightGrad ? dtype_size(g.d_dtype) : es);
-  ProfScope ps(kProfExpertSimt, flops, bytes, s);
-  return expert_simt(g, s) == 0 ? MUON_OK : MUON_ERR_CUDA;
+  const bool tc = expert_tc_ok(g);
+  ProfScope ps(tc ? kProfExpertProduct : kProfExpertSimt, flops, bytes, s);
+  return (tc ? expert_tc(g, s) : expert_simt(g, s)) == 0 ? MUON_OK : MUON_ERR_CUDA;
 }
 
 }  // namespace
