@@ -29,10 +29,19 @@
 // The weight gradient's contraction runs over the segment's tokens, so its last
 // k-block may end inside the next expert's rows.  MMAs cover whole groups of 16
 // tokens; the rows of the last group beyond the segment are zeroed in shared
-// memory in both operands (0 * NaN is NaN) by the producer warps, after the
-// TMA load and before the MMA: that block's load reports to a barrier of its
-// own CTA, and the producers of both CTAs arrive on the leader's "full"
-// barrier once their rows are zero.
+// memory in both operands (0 * NaN is NaN), after the TMA load and before the
+// MMA: that block's load reports to a barrier of its own CTA, on which one more
+// warp waits, and once that warp of both CTAs has zeroed its rows and arrived,
+// the leader's "full" barrier opens.  The producers meanwhile go on to the next
+// tiles (waiting for that load in the producer itself emptied the ring at every
+// tile: 334 against TODO us at 49152 rows over 64 experts of 1408 x 2048).
+//
+// fp32 weight gradients.  The tensor cores truncate when they add to an fp32
+// accumulator, a bias that grows with the length of the sum (2.5e-6 relative
+// at 1024 tokens, TODO).  Where the result is stored in fp32 a tile is therefore
+// summed in runs of 256 tokens, each in a fresh accumulator (two in TMEM), and
+// 16 epilogue warps add the runs in registers with round-to-nearest, 64 sums a
+// thread, while the next run's MMAs go on.
 //
 // Waits are bounded as in the other product kernels.
 #include <algorithm>
@@ -45,15 +54,22 @@ namespace muon {
 namespace tc {
 namespace expk {
 
-constexpr int NSTAGES = 6;
+// per kernel: epilogue warps, threads (producer, MMA, epilogue and, for weight
+// gradients, the zeroing warp) and ring stages
+constexpr int epi_warps(bool out32) { return out32 ? 16 : NUM_EPI_WARPS; }
+constexpr int threads_of(bool wg, bool out32) { return 64 + 32 * epi_warps(out32) + (wg ? 32 : 0); }
+constexpr int stages_of(bool out32) { return out32 ? 5 : 6; }
+constexpr int FOLD_KB = 4;                        // k-blocks of a run of an fp32 weight gradient: 256 tokens
 constexpr int HALF_BYTES = 128 * BK * 2;          // one operand of a stage in one CTA: 16 KB
 constexpr int STAGE2 = 2 * HALF_BYTES;
 constexpr int BOX_BYTES = STAGE_TILE_BYTES;       // one staging box per epilogue warp
 constexpr int TABLE_INTS = 3 * kMaxExperts + 8;   // segment starts, lengths, first tiles
 constexpr int BAR_BYTES = 256;
-constexpr int SMEM = NSTAGES * STAGE2 + NUM_EPI_WARPS * BOX_BYTES + TABLE_INTS * 4 + BAR_BYTES + 1024;
-static_assert(SMEM <= 232448, "shared memory of one CTA");
-static_assert((2 * NSTAGES + 6) * 8 + 8 <= BAR_BYTES, "barrier area");
+constexpr int smem_of(bool out32) {
+  return stages_of(out32) * STAGE2 + epi_warps(out32) * BOX_BYTES + TABLE_INTS * 4 + BAR_BYTES + 1024;
+}
+static_assert(smem_of(false) <= 232448 && smem_of(true) <= 232448, "shared memory of one CTA");
+static_assert((3 * stages_of(false) + 5) * 8 + 8 <= BAR_BYTES, "barrier area");
 
 struct EParams {
   const int* offsets;
@@ -91,6 +107,15 @@ __device__ __forceinline__ void mma2(uint32_t d_tmem, uint64_t adesc, uint64_t b
       "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
 __device__ __forceinline__ void tma_add_3d(const CUtensorMap* map, uint32_t src, int x, int y, int z) {
   asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
@@ -144,24 +169,25 @@ __device__ __forceinline__ ETile find_tile(const EParams& p, const Table& tb, Cu
 }
 
 template <int KIND, int IN_FMT, bool OUT32>
-__global__ void __launch_bounds__(NUM_THREADS, 1)
+__global__ void __launch_bounds__(threads_of(KIND == kWeightGrad, OUT32), 1)
 expert_kernel(const __grid_constant__ EMaps maps, const __grid_constant__ EParams p) {
   static_assert(KIND == kWeightGrad || !OUT32, "fp32 results: weight gradients only");
   constexpr bool WG = KIND == kWeightGrad;
   constexpr bool A_MN = KIND != kForward;   // A is read along its columns
+  constexpr int NSTAGES = stages_of(OUT32), EPI = epi_warps(OUT32);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* staging = smem + NSTAGES * STAGE2;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(staging + NUM_EPI_WARPS * BOX_BYTES);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(staging + EPI * BOX_BYTES);
   uint64_t* full_bar = bars;                     // [NSTAGES] (used in the leader)
   uint64_t* empty_bar = bars + NSTAGES;          // [NSTAGES] (both CTAs)
   uint64_t* tfull_bar = bars + 2 * NSTAGES;      // [2]       (both CTAs)
   uint64_t* tempty_bar = bars + 2 * NSTAGES + 2; // [2]       (used in the leader)
   uint64_t* drain_bar = bars + 2 * NSTAGES + 4;  // [1]
-  uint64_t* tail_bar = bars + 2 * NSTAGES + 5;   // [1]       (both CTAs; weight grad)
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * NSTAGES + 6);
+  uint64_t* tail_bar = bars + 2 * NSTAGES + 5;   // [NSTAGES] (both CTAs; weight grad)
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 3 * NSTAGES + 5);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  int* table = reinterpret_cast<int*>(staging + NUM_EPI_WARPS * BOX_BYTES + BAR_BYTES);
+  int* table = reinterpret_cast<int*>(staging + EPI * BOX_BYTES + BAR_BYTES);
   const Table tb{table, table + kMaxExperts, table + 2 * kMaxExperts};
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -170,15 +196,15 @@ expert_kernel(const __grid_constant__ EMaps maps, const __grid_constant__ EParam
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < NSTAGES; ++s) {
-      mbar_init(smem_u32(&full_bar[s]), WG ? 2 : 1);  // weight grad: the producers of both CTAs arrive
+      mbar_init(smem_u32(&full_bar[s]), WG ? 2 : 1);  // weight grad: both CTAs arrive
       mbar_init(smem_u32(&empty_bar[s]), 1);
+      mbar_init(smem_u32(&tail_bar[s]), 1);
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(smem_u32(&tfull_bar[a]), 1);
-      mbar_init(smem_u32(&tempty_bar[a]), 2 * NUM_EPI_WARPS);
+      mbar_init(smem_u32(&tempty_bar[a]), 2 * EPI);
     }
     mbar_init(smem_u32(drain_bar), 1);
-    mbar_init(smem_u32(tail_bar), 1);
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -230,14 +256,14 @@ expert_kernel(const __grid_constant__ EMaps maps, const __grid_constant__ EParam
 
   if (warp == 0) {
     // ---------------------------------------------------------------- producers (both CTAs)
-    int stage = 0;
-    uint32_t phase = 0, tail_phase = 0;
-    int ok = 1;
-    Cursor cur;
-    for (int t = pair; t < total && ok; t += pairs) {
-      const ETile tl = find_tile<KIND>(p, tb, cur, t);
-      const int f0 = tl.f * 256 + (int)rank * 128;  // this CTA's rows of D
-      if (lane == 0) {
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      Cursor cur;
+      for (int t = pair; t < total && ok; t += pairs) {
+        const ETile tl = find_tile<KIND>(p, tb, cur, t);
+        const int f0 = tl.f * 256 + (int)rank * 128;  // this CTA's rows of D
         if (!WG) {
           const int half = ((tl.tokens + 31) & ~31) >> 1;  // this CTA's tokens
           const int size = half > 64 ? 3 : half > 32 ? 2 : half > 16 ? 1 : 0;
@@ -246,7 +272,7 @@ expert_kernel(const __grid_constant__ EMaps maps, const __grid_constant__ EParam
           const int row0 = tl.lo + tl.t0 + (int)rank * half;
           const int num_kb = (p.K + BK - 1) / BK;
           for (int kb = 0; kb < num_kb; ++kb) {
-            if (!mbar_wait(smem_u32(&empty_bar[stage]), phase ^ 1u, abort_flag, p.timeout_ns)) { ok = 0; break; }
+            if (!mbar_wait(smem_u32(&empty_bar[stage]), phase ^ 1u, abort_flag, p.timeout_ns)) { ok = false; break; }
             if (leader) mbar_expect_tx(smem_u32(&full_bar[stage]), 2 * (HALF_BYTES + b_bytes));
             const uint32_t fb = leader_full + stage * 8;
             const uint32_t sa = smem_u32(smem + stage * STAGE2);
@@ -263,116 +289,192 @@ expert_kernel(const __grid_constant__ EMaps maps, const __grid_constant__ EParam
           const bool narrow = p.C - tl.c * 256 <= 128;
           const int c0 = tl.c * 256 + (int)rank * (narrow ? 64 : 128);  // this CTA's columns of D
           const uint32_t bytes = HALF_BYTES + (narrow ? HALF_BYTES / 2 : HALF_BYTES);
-          const int whole = (tl.len & 15) ? tl.len / BK : (tl.len + BK - 1) / BK;  // k-blocks that need no zeroing
-          for (int kb = 0; kb < whole; ++kb) {
-            if (!mbar_wait(smem_u32(&empty_bar[stage]), phase ^ 1u, abort_flag, p.timeout_ns)) { ok = 0; break; }
-            const uint32_t fb = leader_full + stage * 8;
-            if (leader) mbar_expect_tx(smem_u32(&full_bar[stage]), 2 * bytes);
-            else remote_arrive_cta(fb);
+          const int num_kb = (tl.len + BK - 1) / BK;
+          const int tail_kb = (tl.len & 15) ? num_kb - 1 : num_kb;  // the k-block that the zeroing warp finishes
+          for (int kb = 0; kb < num_kb; ++kb) {
+            if (!mbar_wait(smem_u32(&empty_bar[stage]), phase ^ 1u, abort_flag, p.timeout_ns)) { ok = false; break; }
             const uint32_t sa = smem_u32(smem + stage * STAGE2);
             const int row = tl.lo + kb * BK;
-            tma_load_pair(sa, &maps.a, fb, f0, row, 0);
-            tma_load_pair(sa + BK * 128, &maps.a, fb, f0 + 64, row, 0);
-            tma_load_pair(sa + HALF_BYTES, &maps.b[0], fb, c0, row, 0);
-            if (!narrow) tma_load_pair(sa + HALF_BYTES + BK * 128, &maps.b[0], fb, c0 + 64, row, 0);
-            if (++stage == NSTAGES) { stage = 0; phase ^= 1u; }
-          }
-        }
-      }
-      if (WG) {
-        stage = __shfl_sync(0xffffffffu, stage, 0);
-        phase = __shfl_sync(0xffffffffu, phase, 0);
-        ok = __shfl_sync(0xffffffffu, ok, 0);
-        if (ok && (tl.len & 15)) {
-          // the k-block that ends inside a group of 16 tokens
-          const bool narrow = p.C - tl.c * 256 <= 128;
-          const int c0 = tl.c * 256 + (int)rank * (narrow ? 64 : 128);
-          uint8_t* sm = smem + stage * STAGE2;
-          if (lane == 0) {
-            ok = mbar_wait(smem_u32(&empty_bar[stage]), phase ^ 1u, abort_flag, p.timeout_ns);
-            if (ok) {
-              const uint32_t sa = smem_u32(sm), tbar = smem_u32(tail_bar);
-              const int row = tl.lo + tl.len / BK * BK;
-              mbar_expect_tx(tbar, HALF_BYTES + (narrow ? HALF_BYTES / 2 : HALF_BYTES));
+            if (kb != tail_kb) {
+              const uint32_t fb = leader_full + stage * 8;
+              if (leader) mbar_expect_tx(smem_u32(&full_bar[stage]), 2 * bytes);
+              else remote_arrive_cta(fb);
+              tma_load_pair(sa, &maps.a, fb, f0, row, 0);
+              tma_load_pair(sa + BK * 128, &maps.a, fb, f0 + 64, row, 0);
+              tma_load_pair(sa + HALF_BYTES, &maps.b[0], fb, c0, row, 0);
+              if (!narrow) tma_load_pair(sa + HALF_BYTES + BK * 128, &maps.b[0], fb, c0 + 64, row, 0);
+            } else {
+              const uint32_t tbar = smem_u32(&tail_bar[stage]);
+              mbar_expect_tx(tbar, bytes);
               tma_load_3d(sa, &maps.a, tbar, f0, row, 0);
               tma_load_3d(sa + BK * 128, &maps.a, tbar, f0 + 64, row, 0);
               tma_load_3d(sa + HALF_BYTES, &maps.b[0], tbar, c0, row, 0);
               if (!narrow) tma_load_3d(sa + HALF_BYTES + BK * 128, &maps.b[0], tbar, c0 + 64, row, 0);
-              volatile int never = 0;  // this CTA's own copies: always waited for
-              ok = mbar_wait(tbar, tail_phase, &never, p.timeout_ns);
-              if (!ok) *abort_flag = 1;
-            }
-          }
-          ok = __shfl_sync(0xffffffffu, ok, 0);
-          if (ok) {
-            tail_phase ^= 1u;
-            // rows [rem, rem rounded up to 16) of the four 64-column boxes, 128 bytes each
-            const int rem = tl.len & (BK - 1), upto = (rem + 15) & ~15;
-            const int per = (upto - rem) * 8;  // 16-byte pieces per box
-            for (int i = lane; i < per * 4; i += 32) {
-              const int box = i / per, k = i - box * per;
-              *reinterpret_cast<uint4*>(sm + box * (BK * 128) + (rem + (k >> 3)) * 128 + (k & 7) * 16) = make_uint4(0, 0, 0, 0);
-            }
-            fence_async_smem();  // the MMA reads these rows through the async proxy
-            __syncwarp();
-            if (lane == 0) {
-              if (leader) mbar_arrive(smem_u32(&full_bar[stage]));
-              else remote_arrive(leader_full + stage * 8);
             }
             if (++stage == NSTAGES) { stage = 0; phase ^= 1u; }
           }
         }
       }
+      // no drain needed where all went well: the leader's MMAs consume every
+      // issued stage, and the final cluster barrier keeps this CTA resident
+      // until then.  After an abort, stages may be on their way that nothing
+      // waits for: copies land within microseconds, so both CTAs stay 1 ms.
+      if (!ok) {
+        const uint64_t t0 = global_timer();
+        for (uint32_t i = 0; i < (1u << 24) && global_timer() - t0 < 1000000ull; ++i) {
+        }
+      }
     }
-    // no drain needed here: the leader's MMAs consume every issued stage,
-    // and the final cluster barrier keeps this CTA resident until then
   } else if (warp == 1) {
     // ---------------------------------------------------------------- MMA issuer (leader only)
     if (lane == 0 && leader) {
       int stage = 0;
       uint32_t phase = 0;
-      int it = 0;
+      int it = 0;  // accumulators begun
       bool ok = true;
       Cursor cur;
-      for (int t = pair; t < total && ok; t += pairs, ++it) {
+      for (int t = pair; t < total && ok; t += pairs) {
         const ETile tl = find_tile<KIND>(p, tb, cur, t);
         const int N = WG ? (p.C - tl.c * 256 <= 128 ? 128 : 256) : (tl.tokens + 31) & ~31;
         const uint32_t idesc = make_idesc(IN_FMT, WG ? 1 : 0, 256, N) | (A_MN ? 1u << 15 : 0u);
         const int K = WG ? tl.len : p.K;
         const int num_kb = (K + BK - 1) / BK;
-        const int acc = it & 1;
-        const uint32_t aph = (uint32_t)(it >> 1) & 1u;
-        if (!mbar_wait(smem_u32(&tempty_bar[acc]), aph ^ 1u, abort_flag, p.timeout_ns)) { ok = false; break; }
-        tc_fence_after();
-        const uint32_t d_tmem = tmem_base + (uint32_t)(acc * BN);
-        for (int kb = 0; kb < num_kb; ++kb) {
-          const bool got = WG ? mbar_wait_cluster(smem_u32(&full_bar[stage]), phase, abort_flag, p.timeout_ns)
-                              : mbar_wait(smem_u32(&full_bar[stage]), phase, abort_flag, p.timeout_ns);
-          if (!got) { ok = false; break; }
+        const int run = OUT32 ? FOLD_KB : num_kb;  // k-blocks per accumulator
+        int kb = 0;
+        do {
+          const int acc = it & 1;
+          const uint32_t aph = (uint32_t)(it >> 1) & 1u;
+          ++it;
+          if (!mbar_wait(smem_u32(&tempty_bar[acc]), aph ^ 1u, abort_flag, p.timeout_ns)) { ok = false; break; }
           tc_fence_after();
-          const uint32_t sa = smem_u32(smem + stage * STAGE2);
-          const uint32_t sb = sa + HALF_BYTES;
-          // groups of 16 that hold a token (weight grad); elsewhere TMA zero-fills the ends of K
-          const int steps = WG ? min(BK / UMMA_K, (K - kb * BK + UMMA_K - 1) / UMMA_K) : BK / UMMA_K;
+          const uint32_t d_tmem = tmem_base + (uint32_t)(acc * BN);
+          const int first = kb, end = min(num_kb, kb + run);
+          for (; kb < end; ++kb) {
+            const bool got = WG ? mbar_wait_cluster(smem_u32(&full_bar[stage]), phase, abort_flag, p.timeout_ns)
+                                : mbar_wait(smem_u32(&full_bar[stage]), phase, abort_flag, p.timeout_ns);
+            if (!got) { ok = false; break; }
+            tc_fence_after();
+            const uint32_t sa = smem_u32(smem + stage * STAGE2);
+            const uint32_t sb = sa + HALF_BYTES;
+            // groups of 16 that hold a token (weight grad); elsewhere TMA zero-fills the ends of K
+            const int steps = WG ? min(BK / UMMA_K, (K - kb * BK + UMMA_K - 1) / UMMA_K) : BK / UMMA_K;
 #pragma unroll
-          for (int k = 0; k < BK / UMMA_K; ++k) {
-            if (k >= steps) break;
-            const uint64_t ad = A_MN ? smem_desc(sa + k * (UMMA_K * 128), BK * 128, 1024)
-                                     : smem_desc(sa + k * (UMMA_K * 2), 16, 1024);
-            const uint64_t bd = WG ? smem_desc(sb + k * (UMMA_K * 128), BK * 128, 1024)
-                                   : smem_desc(sb + k * (UMMA_K * 2), 16, 1024);
-            mma2(d_tmem, ad, bd, idesc, (kb | k) != 0);
+            for (int k = 0; k < BK / UMMA_K; ++k) {
+              if (k >= steps) break;
+              const uint64_t ad = A_MN ? smem_desc(sa + k * (UMMA_K * 128), BK * 128, 1024)
+                                       : smem_desc(sa + k * (UMMA_K * 2), 16, 1024);
+              const uint64_t bd = WG ? smem_desc(sb + k * (UMMA_K * 128), BK * 128, 1024)
+                                     : smem_desc(sb + k * (UMMA_K * 2), 16, 1024);
+              mma2(d_tmem, ad, bd, idesc, kb > first || k > 0);
+            }
+            commit_pair(smem_u32(&empty_bar[stage]), 0x3);  // stage free in both CTAs
+            if (++stage == NSTAGES) { stage = 0; phase ^= 1u; }
           }
-          commit_pair(smem_u32(&empty_bar[stage]), 0x3);  // stage free in both CTAs
-          if (++stage == NSTAGES) { stage = 0; phase ^= 1u; }
-        }
-        if (!ok) break;
-        commit_pair(smem_u32(&tfull_bar[acc]), 0x3);      // accumulator ready in both CTAs
+          if (!ok) break;
+          commit_pair(smem_u32(&tfull_bar[acc]), 0x3);      // accumulator ready in both CTAs
+        } while (kb < num_kb);
       }
       commit_pair(smem_u32(drain_bar), 0x1);
       volatile int never = 0;
       mbar_wait(smem_u32(drain_bar), 0, &never, p.timeout_ns);
     }
+  } else if (WG && warp == 2 + EPI) {
+    // ---------------------------------------------------------------- zeroing of the segments' ends (both CTAs)
+    int stage = 0;
+    uint32_t seen = 0;  // per stage: parity of its next tail load
+    Cursor cur;
+    for (int t = pair; t < total; t += pairs) {
+      const ETile tl = find_tile<KIND>(p, tb, cur, t);
+      const int num_kb = (tl.len + BK - 1) / BK;
+      if (tl.len & 15) {
+        const int s = (stage + num_kb - 1) % NSTAGES;
+        int ok = 1;
+        if (lane == 0) ok = mbar_wait(smem_u32(&tail_bar[s]), (seen >> s) & 1u, abort_flag, p.timeout_ns);
+        if (!__shfl_sync(0xffffffffu, ok, 0)) break;
+        __syncwarp();
+        seen ^= 1u << s;
+        // rows [rem, rem rounded up to 16) of the four 64-column boxes, 128 bytes each
+        uint8_t* sm = smem + s * STAGE2;
+        const int rem = tl.len & (BK - 1), upto = (rem + 15) & ~15;
+        const int per = (upto - rem) * 8;  // 16-byte pieces per box
+        for (int i = lane; i < per * 4; i += 32) {
+          const int box = i / per, k = i - box * per;
+          *reinterpret_cast<uint4*>(sm + box * (BK * 128) + (rem + (k >> 3)) * 128 + (k & 7) * 16) = make_uint4(0, 0, 0, 0);
+        }
+        fence_async_smem();  // the MMA reads these rows through the async proxy
+        __syncwarp();
+        if (lane == 0) {
+          if (leader) mbar_arrive(smem_u32(&full_bar[s]));
+          else remote_arrive(leader_full + s * 8);
+        }
+      }
+      stage = (stage + num_kb) % NSTAGES;
+    }
+  } else if (OUT32) {
+    // ---------------------------------------------------------------- fp32 epilogue (both CTAs): runs added in registers
+    const int q = warp & 3;         // TMEM lane quarter
+    const int c0 = (warp - 2) >> 2 << 6;  // this warp's 64 columns
+    uint8_t* S = staging + (warp - 2) * BOX_BYTES;
+    const uint32_t s0 = smem_u32(S);
+    int it = 0;
+    int ok = 1;
+    Cursor cur;
+    for (int t = pair; t < total && ok; t += pairs) {
+      const ETile tl = find_tile<KIND>(p, tb, cur, t);
+      const int fi = tl.f * 256 + (int)rank * 128 + q * 32;  // first row of D of this warp
+      const int gj = tl.c * 256 + c0;
+      const bool mine = fi < p.F && gj < p.C;
+      const int runs = max(1, (tl.len + FOLD_KB * BK - 1) / (FOLD_KB * BK));
+      float sum[64];
+#pragma unroll
+      for (int j = 0; j < 64; ++j) sum[j] = 0.f;
+      for (int run = 0; run < runs; ++run, ++it) {
+        const int acc = it & 1;
+        const uint32_t aph = (uint32_t)(it >> 1) & 1u;
+        if (lane == 0) ok = mbar_wait(smem_u32(&tfull_bar[acc]), aph, abort_flag, p.timeout_ns);
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        if (!ok) break;
+        tc_fence_after();
+        if (mine && tl.len > 0) {
+          const uint32_t tbase = tmem_base + (uint32_t)(acc * BN + c0) + ((uint32_t)(q * 32) << 16);
+#pragma unroll
+          for (int h = 0; h < 4; ++h) {
+            uint32_t r[16];
+            tmem_ld16(tbase + h * 16, r);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) sum[h * 16 + j] += __uint_as_float(r[j]);
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if (leader) mbar_arrive(smem_u32(&tempty_bar[acc]));
+          else remote_arrive_cta(leader_tempty + acc * 8);
+        }
+      }
+      if (!ok || !mine) continue;
+      // boxes of 16 columns
+#pragma unroll
+      for (int h = 0; h < 4; ++h) {
+        if (gj + h * 16 >= p.C) break;
+        if (lane == 0) bulk_wait_read0();
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          *reinterpret_cast<float4*>(S + sw64(lane, k)) =
+              make_float4(sum[h * 16 + k * 4], sum[h * 16 + k * 4 + 1], sum[h * 16 + k * 4 + 2], sum[h * 16 + k * 4 + 3]);
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          if (p.accumulate) tma_add_3d(&maps.d, s0, gj + h * 16, fi, tl.e);
+          else tma_store_3d(&maps.d, s0, gj + h * 16, fi, tl.e);
+          bulk_commit();
+        }
+      }
+    }
+    __syncwarp();
+    if (lane == 0) bulk_wait_all0();  // this warp's output stores have completed
+    __syncwarp();
   } else {
     // ---------------------------------------------------------------- epilogue (both CTAs)
     const int q = warp & 3;            // TMEM lane quarter
@@ -411,85 +513,63 @@ expert_kernel(const __grid_constant__ EMaps maps, const __grid_constant__ EParam
 #pragma unroll
           for (int j = 0; j < 32; ++j) r[j] = 0;
         }
-        if (OUT32) {
-          // two boxes of 16 columns
-          const int gj = tl.c * 256 + c * 32;
+        float v[32];
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            if (gj + h * 16 >= p.C) break;
-            if (lane == 0) bulk_wait_read0();
-            __syncwarp();
+        for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
+        uint4 dq[4];
+        pack_row32(v, IN_FMT ? kBF16 : kFP16, dq);
+        if (lane == 0) bulk_wait_read0();  // the box is free once the previous store has read it
+        __syncwarp();
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              *reinterpret_cast<uint4*>(S + sw64(lane, k)) =
-                  make_uint4(r[h * 16 + k * 4], r[h * 16 + k * 4 + 1], r[h * 16 + k * 4 + 2], r[h * 16 + k * 4 + 3]);
-            fence_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-              if (p.accumulate) tma_add_3d(&maps.d, s0, gj + h * 16, fi, tl.e);
-              else tma_store_3d(&maps.d, s0, gj + h * 16, fi, tl.e);
-              bulk_commit();
-            }
+        for (int k = 0; k < 4; ++k) *reinterpret_cast<uint4*>(S + sw64(lane, k)) = dq[k];
+        if (WG) {
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            tma_store_3d(&maps.d, s0, tl.c * 256 + c * 32, fi, tl.e);
+            bulk_commit();
           }
         } else {
-          float v[32];
+          // rows of the box are features: turn it in place, then its rows are tokens
+          __syncwarp();
+          uint32_t m[4][4];
 #pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
-          uint4 dq[4];
-          pack_row32(v, IN_FMT ? kBF16 : kFP16, dq);
-          if (lane == 0) bulk_wait_read0();  // the box is free once the previous store has read it
+          for (int g = 0; g < 4; ++g)
+            asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(m[g][0]), "=r"(m[g][1]), "=r"(m[g][2]), "=r"(m[g][3])
+                         : "r"(s0 + sw64(lane, g))
+                         : "memory");
           __syncwarp();
 #pragma unroll
-          for (int k = 0; k < 4; ++k) *reinterpret_cast<uint4*>(S + sw64(lane, k)) = dq[k];
-          if (WG) {
+          for (int g = 0; g < 4; ++g)
+            asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(
+                             s0 + sw64(g * 8 + (lane & 7), lane >> 3)),
+                         "r"(m[g][0]), "r"(m[g][1]), "r"(m[g][2]), "r"(m[g][3])
+                         : "memory");
+          const int valid = tl.tokens - c * 32;         // tokens of this box that are the expert's
+          const int row = tl.lo + tl.t0 + c * 32;
+          if (valid >= 32) {
             fence_async_smem();
             __syncwarp();
             if (lane == 0) {
-              tma_store_3d(&maps.d, s0, tl.c * 256 + c * 32, fi, tl.e);
+              tma_store_3d(&maps.d, s0, fi, row, 0);    // clips the features past F
               bulk_commit();
             }
           } else {
-            // rows of the box are features: turn it in place, then its rows are tokens
-            __syncwarp();
-            uint32_t m[4][4];
-#pragma unroll
-            for (int g = 0; g < 4; ++g)
-              asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
-                           : "=r"(m[g][0]), "=r"(m[g][1]), "=r"(m[g][2]), "=r"(m[g][3])
-                           : "r"(s0 + sw64(lane, g))
-                           : "memory");
             __syncwarp();
 #pragma unroll
-            for (int g = 0; g < 4; ++g)
-              asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(
-                               s0 + sw64(g * 8 + (lane & 7), lane >> 3)),
-                           "r"(m[g][0]), "r"(m[g][1]), "r"(m[g][2]), "r"(m[g][3])
-                           : "memory");
-            const int valid = tl.tokens - c * 32;         // tokens of this box that are the expert's
-            const int row = tl.lo + tl.t0 + c * 32;
-            if (valid >= 32) {
-              fence_async_smem();
-              __syncwarp();
-              if (lane == 0) {
-                tma_store_3d(&maps.d, s0, fi, row, 0);    // clips the features past F
-                bulk_commit();
-              }
-            } else {
-              __syncwarp();
+            for (int i = 0; i < 4; ++i) {
+              const int tr = i * 8 + (lane >> 2), f = fi + (lane & 3) * 8;
+              if (tr >= valid || f >= p.F) continue;
+              const uint4 v8 = *reinterpret_cast<const uint4*>(S + sw64(tr, lane & 3));
+              uint16_t* dst = reinterpret_cast<uint16_t*>(p.D) + (long long)(row + tr) * p.ldd + f;
+              if (f + 8 <= p.F) {
+                *reinterpret_cast<uint4*>(dst) = v8;
+              } else {
+                const uint16_t* e = reinterpret_cast<const uint16_t*>(&v8);
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const int tr = i * 8 + (lane >> 2), f = fi + (lane & 3) * 8;
-                if (tr >= valid || f >= p.F) continue;
-                const uint4 v8 = *reinterpret_cast<const uint4*>(S + sw64(tr, lane & 3));
-                uint16_t* dst = reinterpret_cast<uint16_t*>(p.D) + (long long)(row + tr) * p.ldd + f;
-                if (f + 8 <= p.F) {
-                  *reinterpret_cast<uint4*>(dst) = v8;
-                } else {
-                  const uint16_t* e = reinterpret_cast<const uint16_t*>(&v8);
-#pragma unroll
-                  for (int k = 0; k < 8; ++k)
-                    if (f + k < p.F) dst[k] = e[k];
-                }
+                for (int k = 0; k < 8; ++k)
+                  if (f + k < p.F) dst[k] = e[k];
               }
             }
           }
@@ -532,14 +612,15 @@ static int launch(const EMaps& maps, const EParams& p, long long tiles, cudaStre
   attr[0].val.clusterDim.x = 2;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
-  cfg.blockDim = dim3(NUM_THREADS);
-  cfg.dynamicSmemBytes = SMEM;
+  constexpr int smem = smem_of(OUT32);
+  cfg.blockDim = dim3(threads_of(KIND == kWeightGrad, OUT32));
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   int max_pairs = max_pairs_of[dev].load(std::memory_order_acquire);
   if (max_pairs <= 0) {
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return (int)e;
     cfg.gridDim = dim3(2 * (num_sms() / 2));
     int n = 0;
