@@ -144,16 +144,18 @@ MUON_API size_t muon_workspace_min(const muon_group* groups, int n_groups, const
 MUON_API int muon_step(const muon_group* groups, int n_groups, const muon_hparams* hp, void* ws, size_t ws_bytes,
               int* status_per_matrix, void* stream);
 
-/* One group of `count` blocks that share a shape rows x cols, each a part of a
- * larger row-major matrix: a head's rows of an attention projection, its
- * columns of the output projection, gate or up of a fused weight, an expert of
- * a stack.  As muon_group, with the row pitch (in elements, at least cols) of
- * the matrices that the blocks lie in, and pointers that need no more than
- * their elements' alignment (rows that all start on 16 bytes are moved by
- * 16-byte accesses, others element by element).  Nothing outside the blocks is
- * read or written; blocks of one call must not overlap. */
+/* One group of `count` row-major matrices, each tiled by down x across blocks
+ * of rows x cols: a head's rows of an attention projection, its columns of the
+ * output projection, gate and up of a fused weight, the experts of a stack.  As
+ * muon_group, with the row pitch (in elements, at least across * cols) of the
+ * matrices, and pointers that need no more than their elements' alignment
+ * (rows that all start on 16 bytes are moved by 16-byte accesses, others element
+ * by element).  Nothing outside the blocks is read or written; blocks of one
+ * call must not overlap.  Blocks count in the order of the groups, their
+ * matrices, block rows and block columns. */
 typedef struct {
   int rows, cols, count;
+  int down, across;
   int w_dtype, g_dtype;
   long long ld_w, ld_g, ld_m;
   void* const* W;

@@ -48,6 +48,8 @@ EXPERT_MAX = 1024
 NOALLOC_SCRATCH_BYTES = 64 << 20
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 _LIB = None
 
 
@@ -70,7 +72,7 @@ class _Group(ctypes.Structure):
 
 class _BlockGroup(ctypes.Structure):
     _fields_ = [("rows", ctypes.c_int), ("cols", ctypes.c_int), ("count", ctypes.c_int),
-                ("w_dtype", ctypes.c_int), ("g_dtype", ctypes.c_int),
+                ("down", ctypes.c_int), ("across", ctypes.c_int), ("w_dtype", ctypes.c_int), ("g_dtype", ctypes.c_int),
                 ("ld_w", ctypes.c_longlong), ("ld_g", ctypes.c_longlong), ("ld_m", ctypes.c_longlong),
                 ("W", ctypes.POINTER(ctypes.c_void_p)), ("G", ctypes.POINTER(ctypes.c_void_p)),
                 ("M", ctypes.POINTER(ctypes.c_void_p))]
@@ -178,21 +180,24 @@ def _stream_handle(stream) -> int:
     return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
 
 
-def _on(device: torch.device, stream, call):
-    """call(stream handle) with ``device`` current and, if a stream is given, that
+def _elsewhere(device: torch.device, stream, call, *args, **kw):
+    """call(*args, **kw) with ``device`` current and, if a stream is given, that
     stream current too, so that what the call allocates belongs to it."""
-    if stream is None and device.index == torch.cuda.current_device():
-        return call(torch.cuda.current_stream(device).cuda_stream)
     with torch.cuda.device(device):
         if stream is None:
-            return call(torch.cuda.current_stream(device).cuda_stream)
+            return call(*args, **kw)
         if not hasattr(stream, "cuda_stream"):
             handle = int(stream)
             stream = torch.cuda.ExternalStream(handle, device=device) if handle else torch.cuda.default_stream(device)
         if stream.device != device:
             raise MuonError(f"the stream is on {stream.device}, the tensors on {device}")
         with torch.cuda.stream(stream):
-            return call(stream.cuda_stream)
+            return call(*args, **kw)
+
+
+def _here(device: torch.device, stream) -> bool:
+    """Whether a call on ``device`` can go out as things are: no stream asked for, the device current."""
+    return stream is None and device.index == torch.cuda.current_device()
 
 
 def _check_cuda(t: torch.Tensor, name: str):
@@ -238,20 +243,22 @@ def _build_groups(params, grads, moms):
     return groups, len(keys), keep, order
 
 
-def _matrices(t: torch.Tensor, es: int):
+def _matrices(t: torch.Tensor):
     """Addresses of the matrices of (..., R, C), in order."""
-    at = [t.data_ptr()]
+    at, es = [t.data_ptr()], t.element_size()
     for n, stride in zip(t.shape[:-2], t.stride()[:-2]):
-        at = [p + i * stride * es for p in at for i in range(n)]
+        at = [p + o for p in at for o in range(0, n * stride * es, stride * es)] if stride else at * n
     return at
 
 
 def _pitch(t: torch.Tensor, name: str) -> int:
     """The row pitch (in elements) of a matrix, or of the matrices of (..., R, C)."""
-    rows, cols = t.shape[-2:]
-    if cols > 1 and t.stride(-1) != 1:
+    *_, rows, cols = t.shape
+    *_, ld, one = t.stride()
+    if one != 1 and cols > 1:
         raise MuonError(f"{name} must have contiguous rows")
-    ld = t.stride(-2) if rows > 1 else cols
+    if rows <= 1:
+        return cols
     if ld < cols:
         raise MuonError(f"{name} has overlapping rows")
     return ld
@@ -263,11 +270,13 @@ def _build_block_groups(params, grads, moms, blocks):
     columns)."""
     if len(blocks) != len(params):
         raise MuonError("blocks must have one entry per parameter")
-    keys, index, total = [], {}, 0
+    index, total = {}, 0
     for w, g, m, block in zip(params, grads, moms, blocks):
         for t, name in ((w, "param"), (g, "grad"), (m, "momentum")):
             if not t.is_cuda:
                 raise MuonError(f"{name} must be a CUDA tensor")
+            if t.device != params[0].device:
+                raise MuonError(f"{name} is on {t.device}, not on {params[0].device}")
             if t.dim() < 2 or t.numel() == 0:
                 raise MuonError(f"{name} must have at least two dimensions and no empty one")
         if w.shape != g.shape or w.shape != m.shape:
@@ -278,29 +287,22 @@ def _build_block_groups(params, grads, moms, blocks):
         r, c = (rows, cols) if block is None else (int(block[0]), int(block[1]))
         if r < 1 or c < 1 or rows % r or cols % c:
             raise MuonError(f"blocks of {r} x {c} do not tile a {rows} x {cols} matrix")
-        k = (r, c, _dtype_code(w.dtype), _dtype_code(g.dtype)) + tuple(
-            _pitch(t, n) for t, n in ((w, "param"), (g, "grad"), (m, "momentum")))
-        if k not in index:
-            index[k] = len(keys)
-            keys.append((k, [], [], [], []))
-        entry = keys[index[k]]
-        n = 0
-        for t, ld, out in zip((w, g, m), k[4:], entry[1:4]):
-            es = t.element_size()
-            inside = [(i * ld + j) * es for i in range(0, rows, r) for j in range(0, cols, c)]
-            at = [p + o for p in _matrices(t, es) for o in inside]
-            out.extend(at)
-            n = len(at)
-        entry[4].extend(range(total, total + n))
+        k = (r, c, rows // r, cols // c, _dtype_code(w.dtype), _dtype_code(g.dtype), _pitch(w, "param"),
+             _pitch(g, "grad"), _pitch(m, "momentum"))
+        entry = index.setdefault(k, ([], [], [], []))
+        for t, out in zip((w, g, m), entry):
+            out.extend(_matrices(t))
+        n = w.numel() // (r * c)
+        entry[3].extend(range(total, total + n))
         total += n
-    groups = (_BlockGroup * len(keys))()
+    groups = (_BlockGroup * len(index))()
     keep, order = [], []
-    for gi, (k, *ptrs, idx) in enumerate(keys):
+    for gi, (k, (*ptrs, idx)) in enumerate(index.items()):
         arrays = [(ctypes.c_void_p * len(p))(*p) for p in ptrs]
         keep += arrays
-        groups[gi] = _BlockGroup(k[0], k[1], len(idx), k[2], k[3], *k[4:], *arrays)
+        groups[gi] = _BlockGroup(k[0], k[1], len(ptrs[0]), *k[2:], *arrays)
         order += idx
-    return groups, len(keys), keep, order
+    return groups, len(index), keep, order
 
 
 def _hparams(lr, momentum, weight_decay, scale_coef, nesterov, ns):
@@ -422,16 +424,19 @@ def muon_step_blocks(params: Sequence[torch.Tensor], grads: Sequence[torch.Tenso
     if status is not None and (status.dtype != torch.int32 or status.numel() != len(order) or status.device != device):
         raise MuonError(f"status must be an int32 tensor of {len(order)} words on the parameters' device")
 
-    def call(handle):
-        ws = torch.empty(need, dtype=torch.uint8, device=device) if workspace is None else workspace
-        grouped = None if status is None else torch.empty(len(order), dtype=torch.int32, device=device)
-        _raise(lib.muon_step_blocks(groups, ng, ctypes.byref(h), ws.data_ptr(), ws.numel() * ws.element_size(),
-                                    None if grouped is None else grouped.data_ptr(), handle), "muon_step_blocks")
-        if status is not None:
-            status.view(-1)[torch.tensor(order, device=device)] = grouped
-        return status
-
-    return _on(device, stream, call)
+    if workspace is not None and workspace.device != device:
+        raise MuonError(f"the workspace is on {workspace.device}, the parameters on {device}")
+    if not _here(device, stream):
+        return _elsewhere(device, stream, muon_step_blocks, params, grads, moms, blocks, workspace=workspace,
+                          status=status, **hp)
+    ws = torch.empty(need, dtype=torch.uint8, device=device) if workspace is None else workspace
+    grouped = None if status is None else torch.empty(len(order), dtype=torch.int32, device=device)
+    _raise(lib.muon_step_blocks(groups, ng, ctypes.byref(h), ws.data_ptr(), ws.numel() * ws.element_size(),
+                                None if grouped is None else grouped.data_ptr(), _raw_stream(device.index)),
+           "muon_step_blocks")
+    if status is not None:
+        status.view(-1)[torch.tensor(order, device=device)] = grouped
+    return status
 
 
 def muon_ns_workspace_size(count: int, rows: int, cols: int, coeffs=(QUINTIC,) * 5, mode="standard",
@@ -690,36 +695,38 @@ class StreamedMuonStep:
 # ---------------------------------------------------------------------------
 # expert layers
 # ---------------------------------------------------------------------------
-def _rows_arg(t: torch.Tensor, name: str, device=None, dtype=None, shape=None) -> int:
-    """Checks a 2-D matrix with contiguous rows; returns its row pitch."""
-    if not t.is_cuda:
-        raise MuonError(f"{name} must be a CUDA tensor")
-    if device is not None and t.device != device:
-        raise MuonError(f"{name} is on {t.device}, not on {device}")
-    if t.dim() != 2:
-        raise MuonError(f"{name} must be 2-D")
-    if dtype is not None and t.dtype != dtype:
-        raise MuonError(f"{name} must be {dtype}, not {t.dtype}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
-        raise MuonError(f"{name} must be {tuple(shape)}, not {tuple(t.shape)}")
+_CODES = {torch.bfloat16: BF16, torch.float16: FP16, torch.float32: FP32}
+
+
+def _matrix(t: torch.Tensor, name: str, device: torch.device, dtype: torch.dtype, rows: int, cols: int) -> int:
+    """Checks a rows x cols matrix with contiguous rows; returns its row pitch."""
+    if t.device != device or t.dtype != dtype or t.shape != (rows, cols):
+        raise MuonError(f"{name} must be {dtype} ({rows}, {cols}) on {device}, not {t.dtype} {tuple(t.shape)} on {t.device}")
     return _pitch(t, name)
 
 
-def _slot_arg(slot: torch.Tensor, device=None):
-    if not slot.is_cuda or slot.dtype != torch.int32 or slot.dim() != 2 or not slot.is_contiguous():
-        raise MuonError("slot must be a contiguous 2-D int32 CUDA tensor")
-    if device is not None and slot.device != device:
-        raise MuonError(f"slot is on {slot.device}, not on {device}")
-    if slot.shape[1] < 1:
+def _lead(t: torch.Tensor, name: str):
+    """Checks a call's first matrix: (device, dtype, its code, rows, columns, row pitch)."""
+    if not t.is_cuda or t.dim() != 2:
+        raise MuonError(f"{name} must be a 2-D CUDA tensor")
+    dtype, (rows, cols) = t.dtype, t.shape
+    if dtype not in _CODES:
+        raise MuonError(f"unsupported dtype {dtype}")
+    return t.device, dtype, _CODES[dtype], rows, cols, _pitch(t, name)
+
+
+def _slot_arg(slot: torch.Tensor, device: torch.device):
+    if slot.dtype != torch.int32 or slot.dim() != 2 or not slot.is_contiguous() or slot.device != device:
+        raise MuonError(f"slot must be a contiguous 2-D int32 tensor on {device}")
+    tokens, topk = slot.shape
+    if topk < 1:
         raise MuonError("slot must have at least one column")
-    return slot.shape
+    return tokens, topk
 
 
 def _weights_arg(weights: torch.Tensor, slot: torch.Tensor) -> int:
-    if not weights.is_cuda or weights.device != slot.device or not weights.is_contiguous():
-        raise MuonError("weights must be contiguous and on the slots' device")
-    if weights.shape != slot.shape:
-        raise MuonError(f"weights must be {tuple(slot.shape)}, not {tuple(weights.shape)}")
+    if weights.device != slot.device or not weights.is_contiguous() or weights.shape != slot.shape:
+        raise MuonError(f"weights must be contiguous {tuple(slot.shape)} on the slots' device")
     return _dtype_code(weights.dtype)
 
 
@@ -732,34 +739,32 @@ def muon_expert_sort(ids: torch.Tensor, experts: int, *, workspace: torch.Tensor
     [offsets[e], offsets[e + 1]).  ``slot`` (tokens, topk): the sorted row of an
     assignment, -1 where no expert takes it.  ``source`` (tokens * topk): the
     assignment (token * topk + j) of every sorted row, followed by those that
-    no expert takes.  All int32; the sort is stable.
+    no expert takes.  All int32, parts of one allocation; the sort is stable.
     """
-    lib = load_library()
     if not ids.is_cuda or ids.dim() != 2 or ids.dtype not in (torch.int32, torch.int64):
         raise MuonError("ids must be a 2-D int32 or int64 CUDA tensor")
+    device = ids.device
+    lib = load_library()
     tokens, topk = ids.shape
-    need = int(lib.muon_expert_sort_workspace_size(tokens, topk, experts))
+    need = lib.muon_expert_sort_workspace_size(tokens, topk, experts)
     if need == 0:
         raise MuonError(f"cannot sort {tokens} x {topk} assignments to {experts} experts (workspace query returned 0)")
-    ld = _pitch(ids, "ids")
-    device = ids.device
-
-    def call(handle):
-        # one allocation: offsets, slot and source, each from a 16-byte boundary
-        n, o = tokens * topk, (experts + 4) // 4 * 4
-        p = (n + 3) // 4 * 4
-        out = torch.empty(o + p + n, dtype=torch.int32, device=device)
-        offsets, slot, source = out[:experts + 1], out[o:o + n].view(tokens, topk), out[o + p:]
-        ws = workspace
-        if ws is None and need > 256:
-            ws = torch.empty(need, dtype=torch.uint8, device=device)
-        base = out.data_ptr()
-        _raise(lib.muon_expert_sort(ids.data_ptr(), ids.element_size(), ld, tokens, topk, experts, base, base + 4 * o,
-                                    base + 4 * (o + p), None if ws is None else ws.data_ptr(),
-                                    0 if ws is None else ws.numel() * ws.element_size(), handle), "muon_expert_sort")
-        return offsets, slot, source
-
-    return _on(device, stream, call)
+    ld, n, es = _pitch(ids, "ids"), tokens * topk, ids.element_size()
+    if not _here(device, stream):
+        return _elsewhere(device, stream, muon_expert_sort, ids, experts, workspace=workspace)
+    out = torch.empty(experts + 1 + 2 * n, dtype=torch.int32, device=device)
+    offsets, slot, source = out.split_with_sizes((experts + 1, n, n))
+    ws, ws_bytes = workspace, 0
+    if ws is not None and ws.device != device:
+        raise MuonError(f"the workspace is on {ws.device}, ids on {device}")
+    if ws is None and need > 256:
+        ws = torch.empty(need, dtype=torch.uint8, device=device)
+    if ws is not None:
+        ws, ws_bytes = ws.data_ptr(), ws.numel() * ws.element_size()
+    base = out.data_ptr()
+    _raise(lib.muon_expert_sort(ids.data_ptr(), es, ld, tokens, topk, experts, base, base + 4 * (experts + 1),
+                                base + 4 * (experts + 1 + n), ws, ws_bytes, _raw_stream(device.index)), "muon_expert_sort")
+    return offsets, slot.view(tokens, topk), source
 
 
 def muon_expert_gather(x: torch.Tensor, slot: torch.Tensor, *, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
@@ -769,19 +774,18 @@ def muon_expert_gather(x: torch.Tensor, slot: torch.Tensor, *, out: torch.Tensor
     cols) defaults to a new tensor of one row per assignment; rows that no slot
     names keep their contents, and slots outside it are skipped.
     """
-    lib = load_library()
-    tokens, topk = _slot_arg(slot, x.device)
-    ld = _rows_arg(x, "x", shape=(tokens, x.shape[-1]))
-    cols, dt = x.shape[1], _dtype_code(x.dtype)
-    ld_out = cols if out is None else _rows_arg(out, "out", x.device, x.dtype, (out.shape[0], cols))
-
-    def call(handle):
-        xs = torch.empty(tokens * topk, cols, dtype=x.dtype, device=x.device) if out is None else out
-        _raise(lib.muon_expert_gather(x.data_ptr(), ld, slot.data_ptr(), tokens, topk, cols, dt, xs.data_ptr(), ld_out,
-                                      xs.shape[0], handle), "muon_expert_gather")
-        return xs
-
-    return _on(x.device, stream, call)
+    device, dtype, code, tokens, cols, ld = _lead(x, "x")
+    topk = _slot_arg(slot, device)[1]
+    if slot.shape[0] != tokens:
+        raise MuonError(f"slot must have {tokens} rows, not {slot.shape[0]}")
+    ld_out = cols if out is None else _matrix(out, "out", device, dtype, out.shape[0], cols)
+    if not _here(device, stream):
+        return _elsewhere(device, stream, muon_expert_gather, x, slot, out=out)
+    if out is None:
+        out = torch.empty(tokens * topk, cols, dtype=dtype, device=device)
+    _raise(load_library().muon_expert_gather(x.data_ptr(), ld, slot.data_ptr(), tokens, topk, cols, code, out.data_ptr(),
+                                             ld_out, out.shape[0], _raw_stream(device.index)), "muon_expert_gather")
+    return out
 
 
 def muon_expert_combine(ys: torch.Tensor, slot: torch.Tensor, weights: torch.Tensor | None = None, *,
@@ -791,22 +795,17 @@ def muon_expert_combine(ys: torch.Tensor, slot: torch.Tensor, weights: torch.Ten
     ``weights`` is (tokens, topk) of any supported type (None: ones).  An
     assignment that no expert takes adds nothing, whatever its weight.
     """
-    lib = load_library()
-    tokens, topk = _slot_arg(slot, ys.device)
-    ld = _rows_arg(ys, "ys")
-    rows, cols = ys.shape
-    dt = _dtype_code(ys.dtype)
-    wdt = 0 if weights is None else _weights_arg(weights, slot)
-    ld_out = cols if out is None else _rows_arg(out, "out", ys.device, ys.dtype, (tokens, cols))
-
-    def call(handle):
-        y = torch.empty(tokens, cols, dtype=ys.dtype, device=ys.device) if out is None else out
-        _raise(lib.muon_expert_combine(ys.data_ptr(), ld, rows, slot.data_ptr(),
-                                       None if weights is None else weights.data_ptr(), wdt, tokens, topk, cols, dt,
-                                       y.data_ptr(), ld_out, handle), "muon_expert_combine")
-        return y
-
-    return _on(ys.device, stream, call)
+    device, dtype, code, rows, cols, ld = _lead(ys, "ys")
+    tokens, topk = _slot_arg(slot, device)
+    w, wdt = (None, 0) if weights is None else (weights.data_ptr(), _weights_arg(weights, slot))
+    ld_out = cols if out is None else _matrix(out, "out", device, dtype, tokens, cols)
+    if not _here(device, stream):
+        return _elsewhere(device, stream, muon_expert_combine, ys, slot, weights, out=out)
+    if out is None:
+        out = torch.empty(tokens, cols, dtype=dtype, device=device)
+    _raise(load_library().muon_expert_combine(ys.data_ptr(), ld, rows, slot.data_ptr(), w, wdt, tokens, topk, cols, code,
+                                              out.data_ptr(), ld_out, _raw_stream(device.index)), "muon_expert_combine")
+    return out
 
 
 def muon_expert_gather_backward(dxs: torch.Tensor, slot: torch.Tensor, *, out: torch.Tensor | None = None,
@@ -824,72 +823,48 @@ def muon_expert_combine_backward(dy: torch.Tensor, ys: torch.Tensor, slot: torch
     names keep their contents).  dweights has the weights' type, zero where no
     expert takes the assignment; None if ``weights`` is None.
     """
-    lib = load_library()
-    tokens, topk = _slot_arg(slot, ys.device)
-    ld_ys = _rows_arg(ys, "ys")
-    rows, cols = ys.shape
-    dt = _dtype_code(ys.dtype)
-    ld_dy = _rows_arg(dy, "dy", ys.device, ys.dtype, (tokens, cols))
-    wdt = 0 if weights is None else _weights_arg(weights, slot)
-    ld_out = cols if out is None else _rows_arg(out, "out", ys.device, ys.dtype, (rows, cols))
+    device, dtype, code, rows, cols, ld_ys = _lead(ys, "ys")
+    tokens, topk = _slot_arg(slot, device)
+    ld_dy = _matrix(dy, "dy", device, dtype, tokens, cols)
+    w, wdt, dw, dwp = None, 0, None, None
+    if weights is not None:
+        w, wdt = weights.data_ptr(), _weights_arg(weights, slot)
+    ld_out = cols if out is None else _matrix(out, "out", device, dtype, rows, cols)
+    if not _here(device, stream):
+        return _elsewhere(device, stream, muon_expert_combine_backward, dy, ys, slot, weights, out=out)
+    if out is None:
+        out = torch.empty(rows, cols, dtype=dtype, device=device)
+    if weights is not None:
+        dw = torch.empty_like(weights)
+        dwp = dw.data_ptr()
+    _raise(load_library().muon_expert_combine_backward(
+        dy.data_ptr(), ld_dy, ys.data_ptr(), ld_ys, rows, slot.data_ptr(), w, wdt, tokens, topk, cols, code,
+        out.data_ptr(), ld_out, dwp, _raw_stream(device.index)), "muon_expert_combine_backward")
+    return out, dw
 
-    def call(handle):
-        dys = torch.empty(rows, cols, dtype=ys.dtype, device=ys.device) if out is None else out
-        dw = None if weights is None else torch.empty_like(weights)
-        _raise(lib.muon_expert_combine_backward(dy.data_ptr(), ld_dy, ys.data_ptr(), ld_ys, rows, slot.data_ptr(),
-                                                None if weights is None else weights.data_ptr(), wdt, tokens, topk,
-                                                cols, dt, dys.data_ptr(), ld_out, None if dw is None else dw.data_ptr(),
-                                                handle), "muon_expert_combine_backward")
-        return dys, dw
 
-    return _on(ys.device, stream, call)
-
-
-def _offsets_arg(offsets: torch.Tensor, device) -> int:
-    if not offsets.is_cuda or offsets.device != device or offsets.dtype != torch.int32 or offsets.dim() != 1 or \
-            not offsets.is_contiguous() or offsets.numel() < 2:
+def _offsets_arg(offsets: torch.Tensor, device: torch.device) -> int:
+    if offsets.device != device or offsets.dtype != torch.int32 or offsets.dim() != 1 or \
+            not offsets.is_contiguous() or offsets.shape[0] < 2:
         raise MuonError("offsets must be a contiguous int32 tensor of experts + 1 entries on the rows' device")
-    return offsets.numel() - 1
+    return offsets.shape[0] - 1
 
 
-def _stack_arg(w: torch.Tensor, name: str, experts: int, device, dtype=None):
+def _stack_arg(w: torch.Tensor, name: str, experts: int, device: torch.device, dtype: torch.dtype):
     """(outer, inner, row pitch, expert stride) of an (experts, outer, inner) stack."""
-    if not w.is_cuda or w.device != device or w.dim() != 3 or w.shape[0] != experts:
-        raise MuonError(f"{name} must be ({experts}, outer, inner) on {device}")
-    if dtype is not None and w.dtype != dtype:
-        raise MuonError(f"{name} must be {dtype}, not {w.dtype}")
-    return w.shape[1], w.shape[2], _pitch(w, name), w.stride(0) if experts > 1 else w.shape[1] * w.shape[2]
+    if w.device != device or w.dtype != dtype or w.dim() != 3 or w.shape[0] != experts:
+        raise MuonError(f"{name} must be {dtype} ({experts}, outer, inner) on {device}, not {w.dtype} {tuple(w.shape)} "
+                        f"on {w.device}")
+    _, outer, inner = w.shape
+    return outer, inner, _pitch(w, name), w.stride(0) if experts > 1 else outer * inner
 
 
-def _status_arg(status, device):
+def _status_arg(status, device: torch.device):
     if status is None:
         return None
-    if not status.is_cuda or status.device != device or status.dtype != torch.int32 or status.numel() != 1:
+    if status.device != device or status.dtype != torch.int32 or status.numel() != 1:
         raise MuonError("status must be one int32 word on the rows' device")
     return status.data_ptr()
-
-
-def _expert_rows_product(entry, a, w, offsets, out, status, stream, to_outer):
-    """y = W xs (to_outer) or dxs = W^T dys, for every expert's rows."""
-    lib = load_library()
-    name = "xs" if to_outer else "dys"
-    ld_a = _rows_arg(a, name)
-    rows, width = a.shape
-    experts = _offsets_arg(offsets, a.device)
-    outer, inner, ld_w, stride_w = _stack_arg(w, "w", experts, a.device, a.dtype)
-    if width != (inner if to_outer else outer):
-        raise MuonError(f"{name} must have {inner if to_outer else outer} columns, not {width}")
-    cols, dt = (outer if to_outer else inner), _dtype_code(a.dtype)
-    ld_out = cols if out is None else _rows_arg(out, "out", a.device, a.dtype, (rows, cols))
-    word = _status_arg(status, a.device)
-
-    def call(handle):
-        d = torch.empty(rows, cols, dtype=a.dtype, device=a.device) if out is None else out
-        _raise(getattr(lib, entry)(a.data_ptr(), ld_a, w.data_ptr(), ld_w, stride_w, offsets.data_ptr(), experts, rows,
-                                   inner, outer, dt, d.data_ptr(), ld_out, word, handle), entry)
-        return d
-
-    return _on(a.device, stream, call)
 
 
 def muon_expert_product(xs: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, *, out: torch.Tensor | None = None,
@@ -905,14 +880,42 @@ def muon_expert_product(xs: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor
     address, on the CUDA cores.  ``status``: one int32 word for a device-side
     timeout.
     """
-    return _expert_rows_product("muon_expert_product", xs, w, offsets, out, status, stream, True)
+    device, dtype, code, rows, width, ld = _lead(xs, "xs")
+    experts = _offsets_arg(offsets, device)
+    outer, inner, ld_w, stride_w = _stack_arg(w, "w", experts, device, dtype)
+    if width != inner:
+        raise MuonError(f"xs must have {inner} columns, not {width}")
+    word = _status_arg(status, device)
+    ld_out = outer if out is None else _matrix(out, "out", device, dtype, rows, outer)
+    if not _here(device, stream):
+        return _elsewhere(device, stream, muon_expert_product, xs, w, offsets, out=out, status=status)
+    if out is None:
+        out = torch.empty(rows, outer, dtype=dtype, device=device)
+    _raise(load_library().muon_expert_product(
+        xs.data_ptr(), ld, w.data_ptr(), ld_w, stride_w, offsets.data_ptr(), experts, rows, inner, outer, code,
+        out.data_ptr(), ld_out, word, _raw_stream(device.index)), "muon_expert_product")
+    return out
 
 
 def muon_expert_input_grad(dys: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, *,
                            out: torch.Tensor | None = None, status: torch.Tensor | None = None,
                            stream=None) -> torch.Tensor:
     """The input gradient of muon_expert_product: out[p] = w[e]^T @ dys[p] for expert e's rows p."""
-    return _expert_rows_product("muon_expert_input_grad", dys, w, offsets, out, status, stream, False)
+    device, dtype, code, rows, width, ld = _lead(dys, "dys")
+    experts = _offsets_arg(offsets, device)
+    outer, inner, ld_w, stride_w = _stack_arg(w, "w", experts, device, dtype)
+    if width != outer:
+        raise MuonError(f"dys must have {outer} columns, not {width}")
+    word = _status_arg(status, device)
+    ld_out = inner if out is None else _matrix(out, "out", device, dtype, rows, inner)
+    if not _here(device, stream):
+        return _elsewhere(device, stream, muon_expert_input_grad, dys, w, offsets, out=out, status=status)
+    if out is None:
+        out = torch.empty(rows, inner, dtype=dtype, device=device)
+    _raise(load_library().muon_expert_input_grad(
+        dys.data_ptr(), ld, w.data_ptr(), ld_w, stride_w, offsets.data_ptr(), experts, rows, inner, outer, code,
+        out.data_ptr(), ld_out, word, _raw_stream(device.index)), "muon_expert_input_grad")
+    return out
 
 
 def muon_expert_weight_grad(dys: torch.Tensor, xs: torch.Tensor, offsets: torch.Tensor, *,
@@ -925,35 +928,34 @@ def muon_expert_weight_grad(dys: torch.Tensor, xs: torch.Tensor, offsets: torch.
     matrices are gradients as muon_step and muon_step_blocks take them.
     ``accumulate`` adds to a float32 ``out`` (gradient accumulation).
     """
-    lib = load_library()
-    ld_dys = _rows_arg(dys, "dys")
-    rows, outer = dys.shape
-    ld_xs = _rows_arg(xs, "xs", dys.device, dys.dtype, (rows, xs.shape[-1]))
-    inner, dt = xs.shape[1], _dtype_code(dys.dtype)
-    experts = _offsets_arg(offsets, dys.device)
-    if accumulate and out is None:
-        raise MuonError("accumulate needs out")
-    if out is not None:
+    device, dtype, code, rows, outer, ld_dys = _lead(dys, "dys")
+    inner = xs.shape[-1]
+    ld_xs = _matrix(xs, "xs", device, dtype, rows, inner)
+    experts = _offsets_arg(offsets, device)
+    word = _status_arg(status, device)
+    if out is None:
+        if accumulate:
+            raise MuonError("accumulate needs out")
+        out_dtype = out_dtype or dtype
+        odt = _dtype_code(out_dtype)
+        ld_out, stride_out = inner, outer * inner
+    else:
         if out_dtype not in (None, out.dtype):
             raise MuonError(f"out is {out.dtype}, out_dtype {out_dtype}")
-        if tuple(out.shape) != (experts, outer, inner):
+        odt = _dtype_code(out.dtype)
+        if out.shape != (experts, outer, inner):
             raise MuonError(f"out must be {(experts, outer, inner)}, not {tuple(out.shape)}")
-        _, _, ld_out, stride_out = _stack_arg(out, "out", experts, dys.device)
-        out_dtype = out.dtype
-    else:
-        out_dtype = out_dtype or dys.dtype
-        ld_out, stride_out = inner, outer * inner
-    odt = _dtype_code(out_dtype)
-    word = _status_arg(status, dys.device)
-
-    def call(handle):
-        dw = torch.empty(experts, outer, inner, dtype=out_dtype, device=dys.device) if out is None else out
-        _raise(lib.muon_expert_weight_grad(dys.data_ptr(), ld_dys, xs.data_ptr(), ld_xs, offsets.data_ptr(), experts,
-                                           rows, inner, outer, dt, dw.data_ptr(), ld_out, stride_out, odt,
-                                           int(accumulate), word, handle), "muon_expert_weight_grad")
-        return dw
-
-    return _on(dys.device, stream, call)
+        _, _, ld_out, stride_out = _stack_arg(out, "out", experts, device, out.dtype)
+    if not _here(device, stream):
+        return _elsewhere(device, stream, muon_expert_weight_grad, dys, xs, offsets, out=out, out_dtype=out_dtype,
+                          accumulate=accumulate, status=status)
+    if out is None:
+        out = torch.empty(experts, outer, inner, dtype=out_dtype, device=device)
+    _raise(load_library().muon_expert_weight_grad(
+        dys.data_ptr(), ld_dys, xs.data_ptr(), ld_xs, offsets.data_ptr(), experts, rows, inner, outer, code,
+        out.data_ptr(), ld_out, stride_out, odt, int(accumulate), word,
+        _raw_stream(device.index)), "muon_expert_weight_grad")
+    return out
 
 
 class ExpertMuonStep:
@@ -1011,13 +1013,13 @@ class ExpertMuonStep:
             if offsets.numel() != experts + 1 or dys.shape[-1] != outer or xs.shape[-1] != inner:
                 raise MuonError("a stack's dys, xs and offsets do not fit its experts x outer x inner")
 
-        def call(handle):
-            for (i, e0, e1), grad, step in zip(self.slices, self.grads, self.steps):
-                dys, xs, offsets = factors[i]
-                muon_expert_weight_grad(dys, xs, offsets[e0:e1 + 1], out=grad)
-                step(stream=handle)
-
-        _on(self.device, stream, call)
+        if not _here(self.device, stream):
+            return _elsewhere(self.device, stream, self, factors)
+        handle = _raw_stream(self.device.index)
+        for (i, e0, e1), grad, step in zip(self.slices, self.grads, self.steps):
+            dys, xs, offsets = factors[i]
+            muon_expert_weight_grad(dys, xs, offsets[e0:e1 + 1], out=grad)
+            step(stream=handle)
 
     @property
     def status(self) -> torch.Tensor:

@@ -181,6 +181,12 @@ struct GroupView {
   void* const* dst;        // W or X
 };
 
+// The groups of one call; block groups keep their blocks' pointers here.
+struct Views {
+  std::vector<GroupView> groups;
+  std::vector<std::vector<void*>> blocks;  // W, G, M per block group
+};
+
 std::vector<Batch> plan_groups(const std::vector<GroupView>& groups) {
   const int n_groups = (int)groups.size();
   std::vector<Batch> out;
@@ -794,16 +800,17 @@ bool element_aligned(const void* p, int dtype) {
   return reinterpret_cast<uintptr_t>(p) % (uintptr_t)dtype_size(dtype) == 0;
 }
 
-int check_block_groups(const muon_block_group* groups, int n_groups, const muon_hparams* hp,
-                       std::vector<GroupView>* views) {
+int check_block_groups(const muon_block_group* groups, int n_groups, const muon_hparams* hp, Views* views) {
   if (!groups || n_groups <= 0 || check_hparams(hp) != MUON_OK) return MUON_ERR_INVALID;
+  views->blocks.reserve(3 * (size_t)n_groups);
   for (int g = 0; g < n_groups; ++g) {
     const muon_block_group& G = groups[g];
-    if (G.rows <= 0 || G.cols <= 0 || G.count < 0) return MUON_ERR_INVALID;
+    if (G.rows <= 0 || G.cols <= 0 || G.count < 0 || G.down <= 0 || G.across <= 0) return MUON_ERR_INVALID;
     if ((long long)G.rows * G.cols > (1LL << 34)) return MUON_ERR_INVALID;
+    if ((long long)G.down * G.across > (1 << 20) || (long long)G.down * G.across * G.count > (1 << 20)) return MUON_ERR_INVALID;
     if (!dtype_ok(G.w_dtype) || !dtype_ok(G.g_dtype)) return MUON_ERR_UNSUPPORTED;
     for (const long long ld : {G.ld_w, G.ld_g, G.ld_m})
-      if (ld < G.cols || ld > kMaxPitch) return MUON_ERR_INVALID;
+      if (ld < (long long)G.across * G.cols || ld > kMaxPitch) return MUON_ERR_INVALID;
     if (G.count > 0 && (!G.W || !G.G || !G.M)) return MUON_ERR_INVALID;
     for (int i = 0; i < G.count; ++i) {
       if (!G.W[i] || !G.G[i] || !G.M[i]) return MUON_ERR_INVALID;
@@ -811,7 +818,23 @@ int check_block_groups(const muon_block_group* groups, int n_groups, const muon_
           !element_aligned(G.M[i], MUON_FP32))
         return MUON_ERR_INVALID;
     }
-    views->push_back(GroupView{G.rows, G.cols, G.count, G.g_dtype, G.w_dtype, G.ld_g, G.ld_m, G.ld_w, G.G, G.M, G.W});
+    const int blocks = G.count * G.down * G.across;
+    auto expand = [&](auto base, long long ld, int es) -> void* const* {
+      std::vector<void*> at;
+      at.reserve(blocks);
+      for (int i = 0; i < G.count; ++i)
+        for (int r = 0; r < G.down; ++r)
+          for (int c = 0; c < G.across; ++c)
+            at.push_back(const_cast<char*>(reinterpret_cast<const char*>(base[i])) +
+                         ((long long)r * G.rows * ld + (long long)c * G.cols) * es);
+      views->blocks.push_back(std::move(at));
+      return views->blocks.back().data();
+    };
+    void* const* w = expand(G.W, G.ld_w, dtype_size(G.w_dtype));
+    void* const* gr = expand(G.G, G.ld_g, dtype_size(G.g_dtype));
+    void* const* m = expand(G.M, G.ld_m, 4);
+    views->groups.push_back(GroupView{G.rows, G.cols, blocks, G.g_dtype, G.w_dtype, G.ld_g, G.ld_m, G.ld_w,
+                                      const_cast<const void* const*>(gr), reinterpret_cast<float* const*>(m), w});
   }
   return MUON_OK;
 }
@@ -898,9 +921,9 @@ int muon_step(const muon_group* groups, int n_groups, const muon_hparams* hp, vo
 
 size_t muon_blocks_workspace_size(const muon_block_group* groups, int n_groups, const muon_hparams* hp) {
   try {
-    std::vector<GroupView> views;
+    Views views;
     if (check_block_groups(groups, n_groups, hp, &views) != MUON_OK) return 0;
-    return ws_for(plan_groups(views), &hp->ns, true);
+    return ws_for(plan_groups(views.groups), &hp->ns, true);
   } catch (...) {  // std::bad_alloc: no exception crosses the C ABI
     return 0;
   }
@@ -908,9 +931,9 @@ size_t muon_blocks_workspace_size(const muon_block_group* groups, int n_groups, 
 
 size_t muon_blocks_workspace_min(const muon_block_group* groups, int n_groups, const muon_hparams* hp) {
   try {
-    std::vector<GroupView> views;
+    Views views;
     if (check_block_groups(groups, n_groups, hp, &views) != MUON_OK) return 0;
-    return ws_for(plan_groups(views), &hp->ns, false);
+    return ws_for(plan_groups(views.groups), &hp->ns, false);
   } catch (...) {  // std::bad_alloc: no exception crosses the C ABI
     return 0;
   }
@@ -919,10 +942,10 @@ size_t muon_blocks_workspace_min(const muon_block_group* groups, int n_groups, c
 int muon_step_blocks(const muon_block_group* groups, int n_groups, const muon_hparams* hp, void* ws, size_t ws_bytes,
                      int* status_per_block, void* stream) {
   try {
-    std::vector<GroupView> views;
+    Views views;
     const int rc = check_block_groups(groups, n_groups, hp, &views);
     if (rc != MUON_OK) return rc;
-    return step_views(views, hp, ws, ws_bytes, status_per_block, reinterpret_cast<cudaStream_t>(stream));
+    return step_views(views.groups, hp, ws, ws_bytes, status_per_block, reinterpret_cast<cudaStream_t>(stream));
   } catch (...) {  // std::bad_alloc: no exception crosses the C ABI
     return MUON_ERR_INVALID;
   }

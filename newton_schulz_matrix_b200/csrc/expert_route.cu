@@ -244,113 +244,143 @@ template <typename T> struct Pack<T, 16 / sizeof(T)> {
   }
 };
 
-// A thread owns N columns of a token and adds the token's rows in the order
-// of its assignments, four loads in flight; fp32 sum, rounded once.
+// Combine and its gradients give a token to `wpt` neighbouring warps of a
+// block, which walk its columns together: one warp where there are tokens
+// enough to fill the GPU (no block-wide sum, and a warp's loads of one column
+// step overlap the next's), more where there are few.  Up to kGroup
+// assignments are read at once, their rows and weights kept in registers over
+// the columns; more go in groups of kGroup.
+constexpr int kGroup = 8;
+
+struct Taken {  // up to kGroup assignments of a token
+  int row[kGroup];
+  float w[kGroup];
+};
+__device__ __forceinline__ Taken taken(const RouteArgs& a, long long t, int j0) {
+  Taken r;
+#pragma unroll
+  for (int q = 0; q < kGroup; ++q) {
+    const int j = j0 + q;
+    const int s = j < a.topk ? a.slot[t * a.topk + j] : -1;
+    r.row[q] = s < a.rows ? s : -1;
+    r.w[q] = r.row[q] >= 0 && a.weights != nullptr ? load_any(a.weights, t * a.topk + j, a.w_dtype) : 1.f;
+  }
+  return r;
+}
+
+// The rows are added in the order of the assignments; fp32 sum, rounded once.
 template <typename T, int N>
-__global__ void __launch_bounds__(kRouteThreads)
-expert_combine_kernel(const RouteArgs a, int units) {
+__global__ void __launch_bounds__(512)
+expert_combine_kernel(const RouteArgs a, int units, int wpt) {
   using P = Pack<T, N>;
-  const long long t = (long long)blockIdx.x * blockDim.y + threadIdx.y;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const long long t = ((long long)blockIdx.x * (blockDim.x >> 5) + warp) / wpt;
   if (t >= a.tokens) return;
-  const int* slot = a.slot + t * a.topk;
-  for (int c = blockIdx.y * blockDim.x + threadIdx.x; c < units; c += gridDim.y * blockDim.x) {
+  const int step = 32 * wpt * gridDim.y;
+  const int first = (blockIdx.y * wpt + warp % wpt) * 32 + lane;
+  const T* ys = reinterpret_cast<const T*>(a.by_row);
+  const Taken head = taken(a, t, 0);
+  for (int c = first; c < units; c += step) {
     float acc[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) acc[i] = 0.f;
-    for (int j0 = 0; j0 < a.topk; j0 += 4) {
-      P v[4];
-      bool on[4];
-      float w[4];
+    auto add = [&](const Taken& k) {
+      P v[kGroup];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int j = j0 + q;
-        const int s = j < a.topk ? slot[j] : -1;
-        on[q] = s >= 0 && s < a.rows;
-        if (on[q]) {
-          v[q] = reinterpret_cast<const P*>(reinterpret_cast<const T*>(a.by_row) + (long long)s * a.ld_row)[c];
-          w[q] = a.weights != nullptr ? load_any(a.weights, t * a.topk + j, a.w_dtype) : 1.f;
-        }
-      }
+      for (int q = 0; q < kGroup; ++q)
+        if (k.row[q] >= 0) v[q] = reinterpret_cast<const P*>(ys + (long long)k.row[q] * a.ld_row)[c];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        if (!on[q]) continue;
+      for (int q = 0; q < kGroup; ++q) {
+        if (k.row[q] < 0) continue;
         float f[N];
         v[q].get(f);
 #pragma unroll
-        for (int i = 0; i < N; ++i) acc[i] = fmaf(w[q], f[i], acc[i]);
+        for (int i = 0; i < N; ++i) acc[i] = fmaf(k.w[q], f[i], acc[i]);
       }
-    }
+    };
+    add(head);
+    for (int j0 = kGroup; j0 < a.topk; j0 += kGroup) add(taken(a, t, j0));
     P out;
     out.set(acc);
     reinterpret_cast<P*>(reinterpret_cast<T*>(a.out_token) + t * a.ld_out_token)[c] = out;
   }
 }
 
-// One token per block: dy is read once per kDots assignments, each row of ys
-// once, and every row of dys is written once; the dot products go through a
-// fixed tree (lanes, then warps in order).
-constexpr int kDots = 8;
+// dy is read once per kGroup assignments, each row of ys once, and every row
+// of dys is written once; the dot products go through a fixed tree (a lane's
+// columns, lanes, then the token's warps in order).
 template <typename T, int N>
-__global__ void __launch_bounds__(kRouteThreads)
-expert_combine_backward_kernel(const RouteArgs a, int units) {
+__global__ void __launch_bounds__(512)
+expert_combine_backward_kernel(const RouteArgs a, int units, int wpt) {
   using P = Pack<T, N>;
-  __shared__ float part[kRouteThreads / 32][kDots];
-  const long long t = blockIdx.x;
-  const int* slot = a.slot + t * a.topk;
-  const T* dy = reinterpret_cast<const T*>(a.by_token) + t * a.ld_token;
-  for (int j0 = 0; j0 < a.topk; j0 += kDots) {
-    float dot[kDots], w[kDots];
-    int row[kDots];
+  __shared__ float part[16][kGroup];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = warp % wpt;
+  const long long t = ((long long)blockIdx.x * (blockDim.x >> 5) + warp) / wpt;
+  const bool live = t < a.tokens;
+  const T* dy = reinterpret_cast<const T*>(a.by_token) + (live ? t : 0) * a.ld_token;
+  const T* ys = reinterpret_cast<const T*>(a.by_row);
+  T* dys = reinterpret_cast<T*>(a.out_row);
+  const bool dots = a.dweights != nullptr;
+  for (int j0 = 0; j0 < a.topk; j0 += kGroup) {
+    float dot[kGroup];
 #pragma unroll
-    for (int q = 0; q < kDots; ++q) {
-      const int j = j0 + q;
-      const int s = j < a.topk ? slot[j] : -1;
-      row[q] = s < a.rows ? s : -1;
-      w[q] = row[q] >= 0 && a.weights != nullptr ? load_any(a.weights, t * a.topk + j, a.w_dtype) : 1.f;
-      dot[q] = 0.f;
-    }
-    for (int c = threadIdx.x; c < units; c += blockDim.x) {
-      float g[N];
-      reinterpret_cast<const P*>(dy)[c].get(g);
-      P v[kDots];
-      if (a.dweights != nullptr) {
+    for (int q = 0; q < kGroup; ++q) dot[q] = 0.f;
+    if (live) {
+      const Taken k = taken(a, t, j0);
+      for (int c = sub * 32 + lane; c < units; c += 32 * wpt) {
+        float g[N];
+        reinterpret_cast<const P*>(dy)[c].get(g);
+        P v[kGroup];
+        if (dots) {
 #pragma unroll
-        for (int q = 0; q < kDots; ++q)
-          if (row[q] >= 0)
-            v[q] = reinterpret_cast<const P*>(reinterpret_cast<const T*>(a.by_row) + (long long)row[q] * a.ld_row)[c];
-      }
+          for (int q = 0; q < kGroup; ++q)
+            if (k.row[q] >= 0) v[q] = reinterpret_cast<const P*>(ys + (long long)k.row[q] * a.ld_row)[c];
+        }
 #pragma unroll
-      for (int q = 0; q < kDots; ++q) {
-        if (row[q] < 0) continue;
-        float f[N];
+        for (int q = 0; q < kGroup; ++q) {
+          if (k.row[q] < 0) continue;
+          float f[N];
 #pragma unroll
-        for (int i = 0; i < N; ++i) f[i] = w[q] * g[i];
-        P out;
-        out.set(f);
-        reinterpret_cast<P*>(reinterpret_cast<T*>(a.out_row) + (long long)row[q] * a.ld_out_row)[c] = out;
-        if (a.dweights != nullptr) {
-          v[q].get(f);
+          for (int i = 0; i < N; ++i) f[i] = k.w[q] * g[i];
+          P out;
+          out.set(f);
+          reinterpret_cast<P*>(dys + (long long)k.row[q] * a.ld_out_row)[c] = out;
+          if (dots) {
+            v[q].get(f);
 #pragma unroll
-          for (int i = 0; i < N; ++i) dot[q] = fmaf(g[i], f[i], dot[q]);
+            for (int i = 0; i < N; ++i) dot[q] = fmaf(g[i], f[i], dot[q]);
+          }
         }
       }
     }
-    if (a.dweights == nullptr) continue;
+    if (!dots) continue;
+    float mine = 0.f;  // lane q: assignment j0 + q
 #pragma unroll
-    for (int q = 0; q < kDots; ++q) {
+    for (int q = 0; q < kGroup; ++q) {
       float s = dot[q];
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) s += __shfl_down_sync(0xffffffffu, s, o);
-      if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5][q] = s;
+      for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+      if (lane == q) mine = s;
     }
-    __syncthreads();
-    if (threadIdx.x < kDots && j0 + (int)threadIdx.x < a.topk) {
-      float s = 0.f;
-      for (int k = 0; k < (int)blockDim.x / 32; ++k) s += part[k][threadIdx.x];
-      store_any(a.dweights, t * a.topk + j0 + threadIdx.x, a.w_dtype, s);
+    if (wpt > 1) {
+      if (lane < kGroup) part[warp][lane] = mine;
+      __syncthreads();
+      if (sub == 0 && lane < kGroup)
+        for (int k = 1; k < wpt; ++k) mine += part[warp + k][lane];
+      __syncthreads();
     }
-    __syncthreads();
+    if (live && sub == 0 && lane < kGroup && j0 + lane < a.topk)
+      store_any(a.dweights, t * a.topk + j0 + lane, a.w_dtype, mine);
   }
+}
+
+// Warps per token: enough to give every SM 32 warps, no more than the row has
+// steps of 32 units, at most 16.
+int warps_per_token(int tokens, int units) {
+  const int steps = (units + 31) / 32;
+  int w = 1;
+  while (w < 16 && w < steps && (long long)tokens * w < 32LL * num_sms()) w *= 2;
+  return w;
 }
 
 bool on16(const void* p, long long ld, int es) {
@@ -428,11 +458,11 @@ int launch_expert_combine(const RouteArgs& a, cudaStream_t s) {
   const int es = dtype_size(a.dtype);
   const bool vec = on16(a.by_row, a.ld_row, es) && on16(a.out_token, a.ld_out_token, es) && (long long)a.cols * es % 16 == 0;
   return with_type(a.dtype, vec, [&](auto type, auto n) {
-    const int units = a.cols / n;
-    const dim3 block = route_block(units);
-    dim3 grid((a.tokens + block.y - 1) / block.y);
-    grid.y = column_blocks(grid.x, units, block.x);
-    expert_combine_kernel<decltype(type), decltype(n)::value><<<grid, block, 0, s>>>(a, units);
+    const int units = a.cols / n, wpt = warps_per_token(a.tokens, units);
+    const int warps = std::max(8, wpt);
+    dim3 grid((unsigned)(((long long)a.tokens * wpt + warps - 1) / warps));
+    grid.y = column_blocks(grid.x, units, 32 * wpt);
+    expert_combine_kernel<decltype(type), decltype(n)::value><<<grid, 32 * warps, 0, s>>>(a, units, wpt);
     return (int)cudaGetLastError();
   });
 }
@@ -443,10 +473,10 @@ int launch_expert_combine_backward(const RouteArgs& a, cudaStream_t s) {
   const bool vec = on16(a.by_token, a.ld_token, es) && on16(a.out_row, a.ld_out_row, es) &&
                    (a.dweights == nullptr || on16(a.by_row, a.ld_row, es)) && (long long)a.cols * es % 16 == 0;
   return with_type(a.dtype, vec, [&](auto type, auto n) {
-    const int units = a.cols / n;
-    int threads = 32;
-    while (threads < kRouteThreads && threads < units) threads *= 2;
-    expert_combine_backward_kernel<decltype(type), decltype(n)::value><<<a.tokens, threads, 0, s>>>(a, units);
+    const int units = a.cols / n, wpt = warps_per_token(a.tokens, units);
+    const int warps = std::max(8, wpt);
+    const unsigned grid = (unsigned)(((long long)a.tokens * wpt + warps - 1) / warps);
+    expert_combine_backward_kernel<decltype(type), decltype(n)::value><<<grid, 32 * warps, 0, s>>>(a, units, wpt);
     return (int)cudaGetLastError();
   });
 }

@@ -3,8 +3,10 @@
 // products the tensor cores would round to TF32, and 16-bit ones that TMA
 // cannot address (a base, pitch or stride that is no multiple of 16 bytes).
 //
-// 64 x 64 output tiles, 16-deep k steps through shared memory, a 4 x 4 block
-// of sums per thread.  The tile list is read from the offsets on the device:
+// 64 x 64 output tiles, 32-deep k steps through shared memory (the next step's
+// elements are loaded into registers while this one is multiplied: with few
+// tiles the loads' latency is what counts), a 4 x 4 block of sums per thread.
+// The tile list is read from the offsets on the device:
 // a block walks the experts' tiles of its own index and stride, so nothing
 // waits for the counts on the host.
 #include <algorithm>
@@ -17,7 +19,8 @@ namespace muon {
 namespace {
 
 constexpr int kTB = 64;
-constexpr int kTK = 16;
+constexpr int kTK = 32;
+constexpr int kLoads = kTB * kTK / 256;  // elements of a tile per thread
 
 // Element (i, k) of an operand at p + i * si + k * sk.
 struct Operand {
@@ -26,14 +29,23 @@ struct Operand {
   int rows, depth;
 };
 
-__device__ void load_tile(const Operand& o, int dt, int i0, int k0, float (*s)[kTB + 4]) {
-  // consecutive threads along the operand's contiguous direction
+// This thread's elements of a tile: consecutive threads along the operand's
+// contiguous direction.
+__device__ __forceinline__ int tile_i(const Operand& o, int e) { return o.sk == 1 ? e / kTK : e % kTB; }
+__device__ __forceinline__ int tile_k(const Operand& o, int e) { return o.sk == 1 ? e % kTK : e / kTB; }
+__device__ __forceinline__ void fetch(const Operand& o, int dt, int i0, int k0, float (&r)[kLoads]) {
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
+  for (int q = 0; q < kLoads; ++q) {
     const int e = threadIdx.x + 256 * q;
-    const int i = o.sk == 1 ? e >> 4 : e & 63, k = o.sk == 1 ? e & 15 : e >> 6;
-    const bool in = i0 + i < o.rows && k0 + k < o.depth;
-    s[k][i] = in ? load_any(o.p, (i0 + i) * o.si + (k0 + k) * o.sk, dt) : 0.f;
+    const int i = i0 + tile_i(o, e), k = k0 + tile_k(o, e);
+    r[q] = i < o.rows && k < o.depth ? load_any(o.p, i * o.si + k * o.sk, dt) : 0.f;
+  }
+}
+__device__ __forceinline__ void put(const Operand& o, const float (&r)[kLoads], float (*s)[kTB + 4]) {
+#pragma unroll
+  for (int q = 0; q < kLoads; ++q) {
+    const int e = threadIdx.x + 256 * q;
+    s[tile_k(o, e)][tile_i(o, e)] = r[q];
   }
 }
 
@@ -60,10 +72,17 @@ expert_simt_kernel(const ExpertDesc g) {
       const Operand A = g.kind == kWeightGrad ? Operand{a, 1, g.ld_a, M, K} : Operand{a, g.ld_a, 1, M, K};
       const Operand B = g.kind == kForward ? Operand{b, g.ld_b, 1, N, K} : Operand{b, 1, g.ld_b, N, K};
       float acc[4][4] = {};
+      float ra[kLoads], rb[kLoads];
+      fetch(A, g.dtype, i0, 0, ra);
+      fetch(B, g.dtype, j0, 0, rb);
       for (int k0 = 0; k0 < K; k0 += kTK) {
-        load_tile(A, g.dtype, i0, k0, As);
-        load_tile(B, g.dtype, j0, k0, Bs);
+        put(A, ra, As);
+        put(B, rb, Bs);
         __syncthreads();
+        if (k0 + kTK < K) {
+          fetch(A, g.dtype, i0, k0 + kTK, ra);
+          fetch(B, g.dtype, j0, k0 + kTK, rb);
+        }
 #pragma unroll
         for (int kk = 0; kk < kTK; ++kk) {
           const float4 a4 = *reinterpret_cast<const float4*>(&As[kk][ty * 4]);

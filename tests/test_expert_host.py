@@ -72,10 +72,10 @@ def test_product_refusals(lib):
         assert lib.muon_expert_weight_grad(*dict(wgrad, **change).values(), None) == rc, change
 
 
-def _block_group(ptr=P, rows=64, cols=128, count=2, wdt=0, gdt=0, ld=(256, 256, 256)):
+def _block_group(ptr=P, rows=64, cols=128, count=2, down=1, across=1, wdt=0, gdt=0, ld=(256, 256, 256)):
     arrs = [(ctypes.c_void_p * count)(*[ptr + 2 * 128 * i for i in range(count)]) for _ in range(2)]
     arrs.append((ctypes.c_void_p * count)(*[P + 4 * 128 * i for i in range(count)]))
-    return nsm._BlockGroup(rows, cols, count, wdt, gdt, *ld, *arrs), arrs
+    return nsm._BlockGroup(rows, cols, count, down, across, wdt, gdt, *ld, *arrs), arrs
 
 
 def test_block_step_refusals(lib):
@@ -91,10 +91,14 @@ def test_block_step_refusals(lib):
     assert size == lib.muon_ns_workspace_size(2, 64, 128, ctypes.byref(ns))
     least = lib.muon_blocks_workspace_min((nsm._BlockGroup * 1)(good), 1, ctypes.byref(hp))
     assert least == lib.muon_ns_workspace_size(1, 64, 128, ctypes.byref(ns))
+    tiled, keep1 = _block_group(down=3, across=2)
+    assert lib.muon_blocks_workspace_size((nsm._BlockGroup * 1)(tiled), 1, ctypes.byref(hp)) == \
+        lib.muon_ns_workspace_size(12, 64, 128, ctypes.byref(ns))
     assert call(good, n=0) == -1 and call(good, ws=None) == -1 and call(good, ws=ctypes.c_void_p((1 << 24) + 8)) == -1
     assert call(good, size=1024) == -3
     for kw, rc in ((dict(ptr=P + 1), -1), (dict(rows=0), -1), (dict(cols=-1), -1), (dict(wdt=3), -2), (dict(gdt=-1), -2),
-                   (dict(ld=(127, 256, 256)), -1), (dict(ld=(256, 0, 256)), -1), (dict(ld=(256, 256, 1 << 31)), -1)):
+                   (dict(ld=(127, 256, 256)), -1), (dict(down=0), -1), (dict(across=-1), -1), (dict(across=3), -1),
+                   (dict(down=1 << 20), -1), (dict(down=1 << 16, across=1 << 16, cols=1, ld=(1 << 20,) * 3), -1), (dict(ld=(256, 0, 256)), -1), (dict(ld=(256, 256, 1 << 31)), -1)):
         bad, keep2 = _block_group(**kw)
         assert call(bad) == rc, kw
         assert lib.muon_blocks_workspace_size((nsm._BlockGroup * 1)(bad), 1, ctypes.byref(hp)) == 0
@@ -203,8 +207,7 @@ def test_block_groups_name_every_block_once():
     groups, n, _keep, order = nsm._build_block_groups([w, w], [w, w], [m, m], [(2, 3), None])
     assert n == 2 and order == list(range(10))
     g = groups[0]
-    assert (g.rows, g.cols, g.count, g.ld_w, g.ld_g, g.ld_m) == (2, 3, 8, 10, 10, 6)
-    assert [g.W[i] - P for i in range(8)] == [2 * (100 * e + 10 * i + j) for e in (0, 1) for i in (0, 2) for j in (0, 3)]
-    assert [g.M[i] - P for i in range(8)] == [4 * (24 * e + 6 * i + j) for e in (0, 1) for i in (0, 2) for j in (0, 3)]
+    assert (g.rows, g.cols, g.count, g.down, g.across, g.ld_w, g.ld_g, g.ld_m) == (2, 3, 2, 2, 2, 10, 10, 6)
+    assert [g.W[i] - P for i in range(2)] == [0, 200] and [g.M[i] - P for i in range(2)] == [0, 96]
     g = groups[1]
-    assert (g.rows, g.cols, g.count) == (4, 6, 2) and [g.W[i] - P for i in range(2)] == [0, 200]
+    assert (g.rows, g.cols, g.count, g.down, g.across) == (4, 6, 2, 1, 1) and [g.W[i] - P for i in range(2)] == [0, 200]
