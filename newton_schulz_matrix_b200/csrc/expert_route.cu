@@ -31,7 +31,10 @@ namespace {
 // equal key found with match_any, one add per distinct key), a prefix over the
 // warps and the experts turns the counts into first positions, and pass 2
 // walks the same pieces again and hands positions out in order, so equal keys
-// keep their order and no atomic decides a position.
+// keep their order and no atomic decides a position.  A warp loads kKeys groups
+// of 32 keys at once and, where its piece is no longer, keeps them for pass 2:
+// one group at a time waits for memory at every group (131072 x 8 ids to 64
+// experts: 26.3 us, 24.6 with groups of eight).
 //
 // Up to kSortOneBlock assignments run as one block and one launch; beyond, a
 // first launch counts the keys of up to one run per SM, and every block of the
@@ -40,6 +43,7 @@ constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kSortOneBlock = 8192;
 constexpr int kSortMinRun = 4096;
+constexpr int kKeys = 8;
 
 __device__ __forceinline__ int key_of(const SortArgs& a, int i) {
   const long long at = a.ld == a.topk ? (long long)i : (long long)(i / a.topk) * a.ld + i % a.topk;
@@ -53,7 +57,17 @@ expert_count_kernel(const SortArgs a, int n, int run, int* __restrict__ counts) 
   for (int e = threadIdx.x; e <= a.experts; e += kSortThreads) hist[e] = 0;
   __syncthreads();
   const int first = blockIdx.x * run, last = min(n, first + run);
-  for (int i = first + (int)threadIdx.x; i < last; i += kSortThreads) atomicAdd(&hist[key_of(a, i)], 1);
+  for (int i0 = first + (int)threadIdx.x; i0 < last; i0 += kKeys * kSortThreads) {
+    int key[kKeys];
+#pragma unroll
+    for (int q = 0; q < kKeys; ++q) {
+      const int i = i0 + q * kSortThreads;
+      key[q] = i < last ? key_of(a, i) : -1;
+    }
+#pragma unroll
+    for (int q = 0; q < kKeys; ++q)
+      if (key[q] >= 0) atomicAdd(&hist[key[q]], 1);
+  }
   __syncthreads();
   int* out = counts + (long long)blockIdx.x * (a.experts + 1);
   for (int e = threadIdx.x; e <= a.experts; e += kSortThreads) out[e] = hist[e];
@@ -77,21 +91,38 @@ expert_rank_kernel(const SortArgs a, int n, int run, int warps, const int* __res
   const int piece = ((last - first + warps - 1) / warps + 31) / 32 * 32;
   const int p0 = first + warp * piece, p1 = warp < warps ? min(last, p0 + piece) : p0;
   int* mine = hist + warp * buckets;
-  for (int i0 = p0; i0 < p1; i0 += 32) {
-    const int i = i0 + lane;
-    const int key = i < p1 ? key_of(a, i) : buckets;
-    const unsigned same = __match_any_sync(0xffffffffu, key);
-    if (key < buckets && lane == __ffs(same) - 1) mine[key] += __popc(same);
-    __syncwarp();
+  int key[kKeys];
+  auto load = [&](int i0) {
+#pragma unroll
+    for (int q = 0; q < kKeys; ++q) {
+      const int i = i0 + q * 32 + lane;
+      key[q] = i < p1 ? key_of(a, i) : buckets;
+    }
+  };
+  for (int i0 = p0; i0 < p1; i0 += 32 * kKeys) {
+    load(i0);
+#pragma unroll
+    for (int q = 0; q < kKeys; ++q) {
+      if (i0 + q * 32 >= p1) break;
+      const unsigned same = __match_any_sync(0xffffffffu, key[q]);
+      if (key[q] < buckets && lane == __ffs(same) - 1) mine[key[q]] += __popc(same);
+      __syncwarp();
+    }
   }
   if (gridDim.x > 1) {
-    // integer sums: their order does not matter
-    for (int k = threadIdx.x; k < (int)gridDim.x * buckets; k += kSortThreads) {
-      const int c = counts[k];
-      if (c == 0) continue;
-      const int b = k / buckets, e = k - b * buckets;
-      atomicAdd(&total[e], c);
-      if (b < (int)blockIdx.x) atomicAdd(&before[e], c);
+    // groups of threads share a bucket's column of counts; integer sums, so
+    // their order does not matter
+    const int groups = max(1, kSortThreads / buckets), g = (int)threadIdx.x / buckets;
+    for (int e = threadIdx.x - g * buckets; e < buckets && g < groups; e += groups > 1 ? buckets : kSortThreads) {
+      int all = 0, upto = 0;
+#pragma unroll 8
+      for (int b = g; b < (int)gridDim.x; b += groups) {
+        const int c = counts[b * buckets + e];
+        all += c;
+        upto += b < (int)blockIdx.x ? c : 0;
+      }
+      atomicAdd(&total[e], all);
+      atomicAdd(&before[e], upto);
     }
   }
   __syncthreads();
@@ -138,23 +169,27 @@ expert_rank_kernel(const SortArgs a, int n, int run, int warps, const int* __res
     }
   }
   __syncthreads();
-  for (int i0 = p0; i0 < p1; i0 += 32) {
-    const int i = i0 + lane;
-    const int key = i < p1 ? key_of(a, i) : buckets;
-    const unsigned same = __match_any_sync(0xffffffffu, key);
-    const int leader = __ffs(same) - 1;
-    int at = 0;
-    if (key < buckets && lane == leader) {
-      at = mine[key];
-      mine[key] = at + __popc(same);
+  for (int i0 = p0; i0 < p1; i0 += 32 * kKeys) {
+    if (p1 - p0 > 32 * kKeys) load(i0);
+#pragma unroll
+    for (int q = 0; q < kKeys; ++q) {
+      if (i0 + q * 32 >= p1) break;
+      const int i = i0 + q * 32 + lane;
+      const unsigned same = __match_any_sync(0xffffffffu, key[q]);
+      const int leader = __ffs(same) - 1;
+      int at = 0;
+      if (key[q] < buckets && lane == leader) {
+        at = mine[key[q]];
+        mine[key[q]] = at + __popc(same);
+      }
+      at = __shfl_sync(0xffffffffu, at, leader);
+      at += __popc(same & ((1u << lane) - 1u));
+      if (i < p1) {
+        a.slot[i] = key[q] < E ? at : -1;
+        a.source[at] = i;
+      }
+      __syncwarp();
     }
-    at = __shfl_sync(0xffffffffu, at, leader);
-    at += __popc(same & ((1u << lane) - 1u));
-    if (i < p1) {
-      a.slot[i] = key < E ? at : -1;
-      a.source[at] = i;
-    }
-    __syncwarp();
   }
 }
 
@@ -269,40 +304,52 @@ __device__ __forceinline__ Taken taken(const RouteArgs& a, long long t, int j0) 
 }
 
 // The rows are added in the order of the assignments; fp32 sum, rounded once.
-template <typename T, int N>
+// A thread has U steps of columns in flight: one of 16 bytes, four of one element.
+template <typename T, int N, int U>
 __global__ void __launch_bounds__(512)
 expert_combine_kernel(const RouteArgs a, int units, int wpt) {
   using P = Pack<T, N>;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const long long t = ((long long)blockIdx.x * (blockDim.x >> 5) + warp) / wpt;
   if (t >= a.tokens) return;
-  const int step = 32 * wpt * gridDim.y;
+  const int next = 32 * wpt * gridDim.y, step = next * U;
   const int first = (blockIdx.y * wpt + warp % wpt) * 32 + lane;
   const T* ys = reinterpret_cast<const T*>(a.by_row);
   const Taken head = taken(a, t, 0);
   for (int c = first; c < units; c += step) {
-    float acc[N];
+    float acc[U][N];
 #pragma unroll
-    for (int i = 0; i < N; ++i) acc[i] = 0.f;
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int i = 0; i < N; ++i) acc[u][i] = 0.f;
     auto add = [&](const Taken& k) {
-      P v[kGroup];
+      P v[U][kGroup];
 #pragma unroll
-      for (int q = 0; q < kGroup; ++q)
-        if (k.row[q] >= 0) v[q] = reinterpret_cast<const P*>(ys + (long long)k.row[q] * a.ld_row)[c];
+      for (int u = 0; u < U; ++u)
 #pragma unroll
-      for (int q = 0; q < kGroup; ++q) {
-        if (k.row[q] < 0) continue;
-        float f[N];
-        v[q].get(f);
+        for (int q = 0; q < kGroup; ++q)
+          if (k.row[q] >= 0 && c + u * next < units)
+            v[u][q] = reinterpret_cast<const P*>(ys + (long long)k.row[q] * a.ld_row)[c + u * next];
 #pragma unroll
-        for (int i = 0; i < N; ++i) acc[i] = fmaf(k.w[q], f[i], acc[i]);
-      }
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int q = 0; q < kGroup; ++q) {
+          if (k.row[q] < 0) continue;
+          float f[N];
+          v[u][q].get(f);
+#pragma unroll
+          for (int i = 0; i < N; ++i) acc[u][i] = fmaf(k.w[q], f[i], acc[u][i]);
+        }
     };
     add(head);
     for (int j0 = kGroup; j0 < a.topk; j0 += kGroup) add(taken(a, t, j0));
-    P out;
-    out.set(acc);
-    reinterpret_cast<P*>(reinterpret_cast<T*>(a.out_token) + t * a.ld_out_token)[c] = out;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (c + u * next >= units) break;
+      P out;
+      out.set(acc[u]);
+      reinterpret_cast<P*>(reinterpret_cast<T*>(a.out_token) + t * a.ld_out_token)[c + u * next] = out;
+    }
   }
 }
 
@@ -461,8 +508,9 @@ int launch_expert_combine(const RouteArgs& a, cudaStream_t s) {
     const int units = a.cols / n, wpt = warps_per_token(a.tokens, units);
     const int warps = std::max(8, wpt);
     dim3 grid((unsigned)(((long long)a.tokens * wpt + warps - 1) / warps));
-    grid.y = column_blocks(grid.x, units, 32 * wpt);
-    expert_combine_kernel<decltype(type), decltype(n)::value><<<grid, 32 * warps, 0, s>>>(a, units, wpt);
+    constexpr int N = decltype(n)::value, U = N == 1 ? 4 : 1;
+    grid.y = column_blocks(grid.x, units, 32 * wpt * U);
+    expert_combine_kernel<decltype(type), N, U><<<grid, 32 * warps, 0, s>>>(a, units, wpt);
     return (int)cudaGetLastError();
   });
 }

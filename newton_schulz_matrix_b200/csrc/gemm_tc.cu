@@ -21,6 +21,12 @@
 //                 one output row per thread), polynomial epilogue, stores
 //   TMEM holds two 128x256 fp32 accumulators so the epilogue of tile i
 //   overlaps the main loop of tile i+1.
+// Products with at most 128 columns (the Gram-sized ones of blocks and matrices
+// with n <= 128) run N = 128 MMAs on half the B tile, in a ring of six stages, or
+// of twelve where both operands are the same rows (X X^T: one load serves both);
+// launches overlap the previous kernel's drain (programmatic dependent launch).
+// The iterations on 64 matrices of 128 x 2048 take 44 us each (51 with
+// 256-column tiles throughout and no overlap of the launches).
 // Every mbarrier wait is bounded (global-timer deadline plus a CTA-wide abort
 // flag); on expiry the CTA drains its in-flight copies and MMAs, frees TMEM,
 // raises the timeout bit in the caller's error word and returns.
@@ -35,6 +41,10 @@
 namespace muon {
 namespace tc {
 
+constexpr int MOST_STAGES = 12;
+static_assert(12 * A_BYTES <= STAGES * STAGE_BYTES && 6 * (A_BYTES + B_BYTES / 2) <= STAGES * STAGE_BYTES, "ring");
+static_assert((2 * MOST_STAGES + 5) * 8 + 8 <= 256, "barrier area");
+
 // ------------------------------------------------------------------ kernel
 template <bool B_MN, int IN_FMT, bool SYM>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
@@ -45,18 +55,24 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ 
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* staging = smem + STAGES * STAGE_BYTES;  // per epilogue warp: two 1024-aligned 2 KB boxes
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + STAGES * STAGE_BYTES + STAGING_BYTES);
-  uint64_t* full_bar = bars;                    // [STAGES]
-  uint64_t* empty_bar = bars + STAGES;          // [STAGES]
-  uint64_t* tfull_bar = bars + 2 * STAGES;      // [2]
-  uint64_t* tempty_bar = bars + 2 * STAGES + 2; // [2]
-  uint64_t* drain_bar = bars + 2 * STAGES + 4;  // [1]
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * STAGES + 5);
+  uint64_t* full_bar = bars;                        // [MOST_STAGES]
+  uint64_t* empty_bar = bars + MOST_STAGES;         // [MOST_STAGES]
+  uint64_t* tfull_bar = bars + 2 * MOST_STAGES;     // [2]
+  uint64_t* tempty_bar = bars + 2 * MOST_STAGES + 2;// [2]
+  uint64_t* drain_bar = bars + 2 * MOST_STAGES + 4; // [1]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * MOST_STAGES + 5);
+  // the ring's bytes as four stages of A and 256 columns of B, six of A and
+  // 128 columns, or twelve of A alone where B is the same 128 rows (X X^T)
+  const bool narrow = p.N <= 128;
+  const bool shared_ab = SYM && narrow && p.same_ab;
+  const int stages = shared_ab ? 12 : narrow ? 6 : STAGES;
+  const int stage_bytes = shared_ab ? A_BYTES : narrow ? A_BYTES + B_BYTES / 2 : STAGE_BYTES;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < STAGES; ++s) {
+    for (int s = 0; s < MOST_STAGES; ++s) {
       mbar_init(smem_u32(&full_bar[s]), 1);
       mbar_init(smem_u32(&empty_bar[s]), 1);
     }
@@ -83,6 +99,10 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ 
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  // as in the paired kernel: nothing below reads global memory before the
+  // previous kernel on the stream has finished, the next one may set up now
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const uint32_t tmem_base = *tmem_slot;
   const int num_kb = (p.K + BK - 1) / BK;
 
@@ -91,31 +111,33 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ 
     if (lane == 0) {
       int stage = 0;
       uint32_t phase = 0;
-      uint32_t issued[STAGES];
-      for (int s = 0; s < STAGES; ++s) issued[s] = 0;
+      uint32_t issued[MOST_STAGES];
+      for (int s = 0; s < MOST_STAGES; ++s) issued[s] = 0;
       bool ok = true;
       for (int t = blockIdx.x; t < p.total_tiles && ok; t += gridDim.x) {
         const Tile tl = decode_tile(p, t);
         for (int kb = 0; kb < num_kb; ++kb) {
           if (!mbar_wait(smem_u32(&empty_bar[stage]), phase ^ 1u, abort_flag, p.timeout_ns)) { ok = false; break; }
           const uint32_t fb = smem_u32(&full_bar[stage]);
-          mbar_expect_tx(fb, STAGE_BYTES);
-          const uint32_t sa = smem_u32(smem + stage * STAGE_BYTES);
+          mbar_expect_tx(fb, stage_bytes);
+          const uint32_t sa = smem_u32(smem + stage * stage_bytes);
           const uint32_t sb = sa + A_BYTES;
           tma_load_3d(sa, &tmap_a, fb, kb * BK, tl.tm * BM, tl.b);
-          if (B_MN) {
+          if (shared_ab) {
+          } else if (B_MN) {
 #pragma unroll
-            for (int q = 0; q < BN / 64; ++q) tma_load_3d(sb + q * (BK * 128), &tmap_b, fb, tl.tn * BN + q * 64, kb * BK, tl.b);
+            for (int q = 0; q < BN / 64; ++q)
+              if (q < 2 || !narrow) tma_load_3d(sb + q * (BK * 128), &tmap_b, fb, tl.tn * BN + q * 64, kb * BK, tl.b);
           } else {
             tma_load_3d(sb, &tmap_b, fb, kb * BK, tl.tn * BN, tl.b);
           }
           issued[stage]++;
-          if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+          if (++stage == stages) { stage = 0; phase ^= 1u; }
         }
       }
       if (!ok) {
         // drain: every stage's most recent load must land before the CTA exits
-        for (int s = 0; s < STAGES; ++s)
+        for (int s = 0; s < stages; ++s)
           if (issued[s]) {
             volatile int never = 0;
             mbar_wait(smem_u32(&full_bar[s]), (issued[s] - 1) & 1u, &never, p.timeout_ns);
@@ -125,7 +147,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ 
   } else if (warp == 1) {
     // ---------------------------------------------------------------- MMA issuer
     if (lane == 0) {
-      constexpr uint32_t idesc = make_idesc(IN_FMT, B_MN ? 1 : 0);
+      const uint32_t idesc = make_idesc(IN_FMT, B_MN ? 1 : 0, BM, narrow ? 128 : BN);
       int stage = 0;
       uint32_t phase = 0;
       int it = 0;
@@ -139,8 +161,8 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ 
         for (int kb = 0; kb < num_kb; ++kb) {
           if (!mbar_wait(smem_u32(&full_bar[stage]), phase, abort_flag, p.timeout_ns)) { ok = false; break; }
           tc_fence_after();
-          const uint32_t sa = smem_u32(smem + stage * STAGE_BYTES);
-          const uint32_t sb = sa + A_BYTES;
+          const uint32_t sa = smem_u32(smem + stage * stage_bytes);
+          const uint32_t sb = shared_ab ? sa : sa + A_BYTES;
 #pragma unroll
           for (int k = 0; k < BK / UMMA_K; ++k) {
             const uint64_t ad = smem_desc(sa + k * (UMMA_K * 2), 16, 1024);
@@ -149,7 +171,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ 
             tc_mma(d_tmem, ad, bd, idesc, (kb | k) != 0);
           }
           tc_commit(smem_u32(&empty_bar[stage]));  // slot free once these MMAs retire
-          if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+          if (++stage == stages) { stage = 0; phase ^= 1u; }
         }
         if (!ok) break;
         tc_commit(smem_u32(&tfull_bar[acc]));      // accumulator ready for the epilogue
@@ -170,6 +192,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ 
       const Tile tl = decode_tile(p, t);
       const int acc = it & 1;
       const uint32_t aph = (uint32_t)(it >> 1) & 1u;
+      const int gi = tl.tm * BM + q * 32 + lane;
       int ok = 1;
       if (lane == 0) ok = mbar_wait(smem_u32(&tfull_bar[acc]), aph, abort_flag, p.timeout_ns);
       ok = __shfl_sync(0xffffffffu, ok, 0);
@@ -177,7 +200,6 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ 
       tc_fence_after();
       const float f = matrix_scale(p.scale, p.scale_pow, tl.b);
       const uint32_t tbase = tmem_base + (uint32_t)(acc * BN) + ((uint32_t)(q * 32) << 16);
-      const int gi = tl.tm * BM + q * 32 + lane;
 #pragma unroll 1
       for (int cc = 0; cc < 4; ++cc) {
         const int c = half * 4 + cc;
@@ -273,8 +295,17 @@ static int launch(const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorMa
     attr_done[dev].store(1, std::memory_order_release);
   }
   const int grid = p.total_tiles < num_sms() ? p.total_tiles : num_sms();
-  gemm_kernel<B_MN, IN_FMT, SYM><<<grid, NUM_THREADS, SMEM_BYTES, s>>>(ma, mb, md, p);
-  return (int)cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(NUM_THREADS);
+  cfg.dynamicSmemBytes = SMEM_BYTES;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = programmatic_launch() ? 1 : 0;
+  return (int)cudaLaunchKernelEx(&cfg, gemm_kernel<B_MN, IN_FMT, SYM>, ma, mb, md, p);
 }
 
 }  // namespace tc
@@ -309,7 +340,8 @@ double gemm_tc_exec_flops(const GemmDesc& g) {
       for (int c = g.symmetric ? r : 0; c < tn; ++c) per_batch += 256.0 * ((c == tn - 1 && narrow) ? 128 : 256);
   } else {
     const int tm = (g.M + BM - 1) / BM, tn = (g.N + BN - 1) / BN;
-    for (int r = 0; r < tm; ++r) per_batch += (double)(tn - (g.symmetric ? r / 2 : 0)) * BM * BN;
+    const double cols = g.N <= 128 ? 128 : BN;
+    for (int r = 0; r < tm; ++r) per_batch += (double)(tn - (g.symmetric ? r / 2 : 0)) * BM * cols;
   }
   return 2.0 * per_batch * k_pad * g.batch;
 }
@@ -343,6 +375,7 @@ int gemm_tc(const GemmDesc& g, cudaStream_t s) {
   p.timeout_ns = wait_timeout_ns();
   p.tile_counter = g.tile_counter;
   p.static_order = static_tile_order() ? 1 : 0;
+  p.same_ab = g.A == g.B && g.lda == g.ldb && g.a_bs == g.b_bs && g.b_kmajor;
 
   if (use_pair_kernel(g)) return gemm_tc_pair(g, p, s);
   if (g.update != nullptr) return (int)cudaErrorInvalidValue;  // the fused update is a paired-kernel epilogue
@@ -353,7 +386,8 @@ int gemm_tc(const GemmDesc& g, cudaStream_t s) {
   if (bmn) {
     if (!encode_map(&mb, g.in_dtype, g.B, g.N, g.K, g.batch, g.ldb, g.b_bs, 64, BK)) return (int)cudaErrorInvalidValue;
   } else {
-    if (!encode_map(&mb, g.in_dtype, g.B, g.K, g.N, g.batch, g.ldb, g.b_bs, BK, BN)) return (int)cudaErrorInvalidValue;
+    if (!encode_map(&mb, g.in_dtype, g.B, g.K, g.N, g.batch, g.ldb, g.b_bs, BK, g.N <= 128 ? 128 : BN))
+      return (int)cudaErrorInvalidValue;
   }
   CUtensorMap md;
   if (!encode_out_map(&md, g)) return (int)cudaErrorInvalidValue;
@@ -364,6 +398,14 @@ int gemm_tc(const GemmDesc& g, cudaStream_t s) {
   }
   if (bmn) return fmt ? launch<true, 1, false>(ma, mb, md, p, s) : launch<true, 0, false>(ma, mb, md, p, s);
   return fmt ? launch<false, 1, false>(ma, mb, md, p, s) : launch<false, 0, false>(ma, mb, md, p, s);
+}
+
+bool tc::programmatic_launch() {
+  static const bool on = [] {
+    const char* e = getenv("MUON_PDL");
+    return !(e && e[0] == '0');
+  }();
+  return on;
 }
 
 bool tc::static_tile_order() {

@@ -335,16 +335,6 @@ gemm_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_consta
   if (threadIdx.x == 0 && *abort_flag && p.err != nullptr) atomicOr(p.err, kStatusTimeout);
 }
 
-// Product launches may start while the previous kernel on the stream drains
-// (programmatic dependent launch); MUON_PDL=0 launches them fully serialised.
-static bool programmatic_launch() {
-  static const bool on = [] {
-    const char* e = getenv("MUON_PDL");
-    return !(e && e[0] == '0');
-  }();
-  return on;
-}
-
 template <bool B_MN, int IN_FMT, bool SYM, bool UPD = false, typename Slots = NoUpdate>
 static int launch(const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorMap& md, const Params& p,
                   cudaStream_t s, const Slots& u = Slots{}) {

@@ -39,6 +39,7 @@ struct Params {
   int* err;
   long long timeout_ns;
   int* tile_counter;      // paired-CTA kernel: device word, 0 at launch; tiles are taken from it in order
+  int same_ab;            // both operands are the same matrix, rows times rows (X X^T)
   int static_order;       // 1: tiles round-robin over the pairs instead (comparison runs)
 };
 
@@ -655,6 +656,10 @@ struct ChainParams {
   long long timeout_ns;
   ChainProduct prod[kMaxProducts];
 };
+
+// Product launches may start while the previous kernel on the stream drains
+// (programmatic dependent launch); MUON_PDL=0 launches them fully serialised.
+bool programmatic_launch();
 
 // Tiles from the counter (default) or round-robin (MUON_TILE_ORDER=static):
 // the same tiles and arithmetic either way, only the hand-out order differs.
