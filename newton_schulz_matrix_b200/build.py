@@ -20,7 +20,7 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libmuon.so")
 SOURCES = ["api.cu", "elementwise.cu", "expert_api.cu", "expert_route.cu", "expert_simt.cu", "expert_tc.cu",
            "gemm_chain.cu", "gemm_simt.cu",
-           "gemm_tc.cu", "gemm_tc2.cu", "gemm_tf32.cu", "noalloc.cu"]
+           "gemm_tc.cu", "gemm_tc2.cu", "gemm_tf32.cu", "noalloc.cu", "ns_block.cu"]
 HEADERS = ["common.cuh", "expert.h", "internal.h", "profile.h", "tc_common.cuh"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",

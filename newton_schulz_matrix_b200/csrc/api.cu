@@ -48,7 +48,7 @@ const char* const kProfNames[kProfKinds] = {"pack_kernel", "norm_kernel", "tc_pr
                                             "gemm_simt_kernel", "unpack_kernel", "ns_fused_small_kernel",
                                             "tc_product[3xtf32]", "tc_chain", "status_or_kernel",
                                             "split_tf32_kernel", "expert_sort", "expert_gather", "expert_combine",
-                                            "expert_combine_backward", "expert_product", "expert_product_simt"};
+                                            "expert_combine_backward", "expert_product", "expert_product_simt", "ns_block_kernel"};
 
 struct Seg {          // `count` matrices of one caller group, starting at index `first`
   int group, first, count;
@@ -618,12 +618,15 @@ bool rows16(const void* const* p, int count, long long ld, int dtype) {
 }
 
 int run_batches(const std::vector<Batch>& batches, const std::vector<GroupView>& views, const std::vector<long long>& first_index,
-                const muon_ns_params* ns, bool update, float mu, int nesterov, float lr, float wd, float scale_coef,
+                const muon_ns_params* ns, bool update, bool blocks, float mu, int nesterov, float lr, float wd, float scale_coef,
                 void* ws, size_t ws_bytes, int* status, cudaStream_t s) {
   for (const Batch& bt : batches) {
     const Layout L = make_layout(bt.n, bt.m, ns);
     if (ws_bytes < chunk_bytes(L, 1)) return MUON_ERR_WORKSPACE;
-    const bool fuse = update && ns->compute_dtype != MUON_FP32 && fused_update_enabled() && gemm_tc_paired(L.n);
+    // small blocks run their whole chain and update in one launch (muon_step keeps the separate products)
+    const bool one_launch = update && blocks && ns->compute_dtype != MUON_FP32 && ns->mode == MUON_NS_STANDARD &&
+                            ns_block_ok(L.n, L.m, ns->iters);
+    const bool fuse = one_launch || (update && ns->compute_dtype != MUON_FP32 && fused_update_enabled() && gemm_tc_paired(L.n));
     int chunk_cap = (int)std::min<size_t>((size_t)bt.total, (ws_bytes - L.fixed) / L.per_matrix);
     if (fuse) chunk_cap = std::min(chunk_cap, UpdateSlots::kMax);
     // slots are assigned in segment order; walk them chunk by chunk
@@ -725,7 +728,14 @@ int run_batches(const std::vector<Batch>& batches, const std::vector<GroupView>&
                                                    (pitch16 && aligned16(v.dst[pc.first + i]) ? 8 : 0));
           }
         }
-        if (run_chain_launch(ctx, L, B, chunk, ns, prescale, &xi, &out_dt, &us) != 0) return MUON_ERR_CUDA;
+        if (one_launch) {
+          const BlockChainArgs ba{L.n, L.m, chunk, ns->iters, prescale ? 0 : 1, cdt, B.X[0], L.ld_m, B.x_bs, B.inv,
+                                  ns->coeffs, B.err};
+          ProfScope ps(kProfBlockChain, flops_of(L.n, L.m, ns) * chunk, 2.0 * chunk * L.n * L.m * 3, s);
+          if (launch_ns_block(ba, us, s) != 0) return MUON_ERR_CUDA;
+        } else if (run_chain_launch(ctx, L, B, chunk, ns, prescale, &xi, &out_dt, &us) != 0) {
+          return MUON_ERR_CUDA;
+        }
         if (status)
           for (const Piece& pc : pieces) {
             ProfScope ps(kProfStatus, 0.0, pc.count * 8.0, s);
@@ -849,8 +859,8 @@ size_t ws_for(const std::vector<Batch>& batches, const muon_ns_params* ns, bool 
 }
 
 // One step over checked groups (muon_step and muon_step_blocks).
-int step_views(const std::vector<GroupView>& views, const muon_hparams* hp, void* ws, size_t ws_bytes, int* status,
-               cudaStream_t s) {
+int step_views(const std::vector<GroupView>& views, bool blocks, const muon_hparams* hp, void* ws, size_t ws_bytes,
+               int* status, cudaStream_t s) {
   if (!ws || (reinterpret_cast<uintptr_t>(ws) & (kAlign - 1))) return MUON_ERR_INVALID;
   std::vector<Batch> batches = plan_groups(views);
   if (ws_bytes < ws_for(batches, &hp->ns, false)) return MUON_ERR_WORKSPACE;
@@ -862,7 +872,7 @@ int step_views(const std::vector<GroupView>& views, const muon_hparams* hp, void
   }
   if (status && total > 0 && cudaMemsetAsync(status, 0, (size_t)total * sizeof(int), s) != cudaSuccess)
     return MUON_ERR_CUDA;
-  return run_batches(batches, views, first, &hp->ns, true, hp->momentum, hp->nesterov, hp->lr, hp->weight_decay,
+  return run_batches(batches, views, first, &hp->ns, true, blocks, hp->momentum, hp->nesterov, hp->lr, hp->weight_decay,
                      hp->scale_coef, ws, ws_bytes, status, s);
 }
 
@@ -916,7 +926,7 @@ int muon_step(const muon_group* groups, int n_groups, const muon_hparams* hp, vo
   std::vector<GroupView> views;
   const int rc = check_groups(groups, n_groups, hp, &views);
   if (rc != MUON_OK) return rc;
-  return step_views(views, hp, ws, ws_bytes, status_per_matrix, reinterpret_cast<cudaStream_t>(stream));
+  return step_views(views, false, hp, ws, ws_bytes, status_per_matrix, reinterpret_cast<cudaStream_t>(stream));
 }
 
 size_t muon_blocks_workspace_size(const muon_block_group* groups, int n_groups, const muon_hparams* hp) {
@@ -945,7 +955,7 @@ int muon_step_blocks(const muon_block_group* groups, int n_groups, const muon_hp
     Views views;
     const int rc = check_block_groups(groups, n_groups, hp, &views);
     if (rc != MUON_OK) return rc;
-    return step_views(views.groups, hp, ws, ws_bytes, status_per_block, reinterpret_cast<cudaStream_t>(stream));
+    return step_views(views.groups, true, hp, ws, ws_bytes, status_per_block, reinterpret_cast<cudaStream_t>(stream));
   } catch (...) {  // std::bad_alloc: no exception crosses the C ABI
     return MUON_ERR_INVALID;
   }
@@ -975,7 +985,7 @@ int muon_ns_batched(void* const* X, int count, int rows, int cols, int dtype, co
   std::vector<long long> first{0};
   if (status_per_matrix && cudaMemsetAsync(status_per_matrix, 0, (size_t)count * sizeof(int), s) != cudaSuccess)
     return MUON_ERR_CUDA;
-  return run_batches(batches, views, first, ns, false, 0.f, 0, 0.f, 0.f, 0.f, ws, ws_bytes, status_per_matrix, s);
+  return run_batches(batches, views, first, ns, false, false, 0.f, 0, 0.f, 0.f, 0.f, ws, ws_bytes, status_per_matrix, s);
 }
 
 double muon_ns_flops(int rows, int cols, const muon_ns_params* ns) {

@@ -153,6 +153,20 @@ constexpr size_t kFusedSmallMaxSmem = 200 * 1024;
 size_t fused_small_smem(int n, int m, int mode);
 int launch_fused_small(const FusedSmallArgs& a, cudaStream_t s);
 
+// Whole 16-bit standard chain and update of blocks with n <= 128 in one launch
+// (ns_block.cu).
+constexpr int kBlockChainMaxIters = 64;
+struct BlockChainArgs {
+  int n, m, count, iters, raw;
+  int dtype;                        // the chain's type
+  const void* x; int ld_x; long long x_bs;
+  const float* inv;
+  const float* coeffs;              // host, 3 * iters
+  int* err;
+};
+bool ns_block_ok(int n, int m, int iters);
+int launch_ns_block(const BlockChainArgs& a, const UpdateSlots& u, cudaStream_t s);
+
 // Per-device caches cover device ordinals below kMaxDevices.
 constexpr int kMaxDevices = 64;
 int current_device();   // -1 on error or an ordinal beyond kMaxDevices

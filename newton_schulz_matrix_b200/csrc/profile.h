@@ -12,7 +12,7 @@ namespace muon {
 enum ProfKind {
   kProfPack, kProfNorm, kProfSyrkTc, kProfGemmTc, kProfGemmSimt, kProfUnpack, kProfFusedSmall, kProfTf32, kProfChain,
   kProfStatus, kProfSplit, kProfExpertSort, kProfExpertGather, kProfExpertCombine, kProfExpertCombineBackward,
-  kProfExpertProduct, kProfExpertSimt, kProfKinds
+  kProfExpertProduct, kProfExpertSimt, kProfBlockChain, kProfKinds
 };
 struct ProfRec {
   int kind;

@@ -1,5 +1,6 @@
 """The Muon step on the blocks of stacked, fused and strided weights: bit for
-bit muon_step on dense copies of the blocks, and nothing outside them moves."""
+bit muon_step on dense copies of the blocks (small blocks, whose chain runs in
+one launch, against the oracle instead), and nothing outside them moves."""
 import math
 
 import pytest
@@ -7,6 +8,7 @@ import torch
 
 import newton_schulz_matrix_b200 as nsm
 import oracle
+import parity_util
 import synth
 
 pytestmark = pytest.mark.gpu
@@ -52,6 +54,26 @@ def make(shape, view, dtype, seed, std):
     return t, store
 
 
+# 16-bit standard chains with n <= 128: one launch, another order of the sums
+ONE_LAUNCH = ("heads", "head-columns", "rows-of-one", "column-of-one")
+
+
+def check_weights(got, w, u, block, chain="fp16", coeffs=None, lr=0.02, wd=0.1):
+    """W against the oracle: decay plus the step, whose O is within the 16-bit bar
+    (2e-2, or 1.25 times what storing in the chain's type costs by itself), and
+    half a step of W's type."""
+    coeffs = coeffs or [oracle.QUINTIC] * 5
+    x = u / (u.norm() + 1e-7)
+    o = torch.from_numpy(oracle.ns_standard((x if block[0] <= block[1] else x.T).numpy(), coeffs))
+    o = o if block[0] <= block[1] else o.T
+    scale = lr * 0.2 * math.sqrt(max(block))
+    ref = (1 - lr * wd) * w - scale * o
+    tol = parity_util.tolerance(chain, parity_util.emulated_floor(u.numpy(), coeffs, "standard", chain=chain))
+    err = float((got.double().cpu() - ref).norm())
+    bound = tol * scale * float(o.norm()) + torch.finfo(got.dtype).eps / 2 * float(ref.norm()) + 1e-12
+    assert err <= bound, (err, bound, tuple(block))
+
+
 @pytest.mark.parametrize("name", sorted(CASES))
 def test_blocks_step_as_dense_copies_do(name):
     shape, block, view, wdt, gdt, hp = CASES[name]
@@ -59,12 +81,19 @@ def test_blocks_step_as_dense_copies_do(name):
                                  make(shape, view, torch.float32, 3, 0.2))
     wd, gd, md = (cut(t, block) for t in (w, g, m))
     before = [t.clone() for t in (ws, gs, ms)]
+    old = [[t.double().cpu() for t in ts] for ts in (wd, gd, md)]
     nsm.muon_step(wd, gd, md, **hp)
     status = torch.full((len(wd),), -1, dtype=torch.int32, device="cuda")
     nsm.muon_step_blocks([w], [g], [m], [block], status=status, **hp)
     assert status.tolist() == [0] * len(wd)
-    for got, want in zip(cut(w, block) + cut(m, block), wd + md):
+    for got, want in zip(cut(m, block), md):
         assert torch.equal(got, want)
+    if name in ONE_LAUNCH:
+        for got, w0, g0, m1 in zip(cut(w, block), old[0], old[1], md):
+            check_weights(got, w0, 0.05 * g0 + 0.95 * m1.double().cpu(), block)
+    else:
+        for got, want in zip(cut(w, block), wd):
+            assert torch.equal(got, want)
     # the storage around the blocks, and G, are as they were
     for t, view_, was in ((ws, w, before[0]), (ms, m, before[2])):
         view_.copy_(torch.zeros_like(view_))
@@ -137,3 +166,63 @@ def test_a_prepared_block_step_captures_and_uses_small_workspaces():
     torch.cuda.current_stream().wait_stream(side)
     for a, b in zip((w, m), want):
         assert torch.equal(a, b)
+
+
+SMALL = [  # block, matrices, coefficients, chain, W type: one, two, four and eight CTAs a block, ragged slices
+    ((128, 2048), 3, None, "fp16", "bf16"), ((2048, 128), 2, None, "fp16", "bf16"), ((64, 512), 2, None, "fp16", "fp32"),
+    ((128, 513), 2, None, "fp16", "fp16"), ((100, 1100), 2, None, "fp16", "bf16"), ((17, 4096), 1, None, "fp16", "bf16"),
+    ((3000, 33), 2, None, "fp16", "bf16"), ((128, 128), 5, None, "fp16", "bf16"), ((1, 640), 2, None, "fp16", "fp32"),
+    ((5, 5), 3, None, "fp16", "bf16"), ((96, 1025), 2, None, "bf16", "bf16"), ((1537, 128), 1, None, "bf16", "fp32"),
+    ((128, 700), 2, [oracle.CUBIC] * 7, "fp16", "bf16"), ((48, 2049), 1, [oracle.QUINTIC], "fp16", "fp32"),
+    ((128, 1536), 2, [oracle.QUINTIC, oracle.CUBIC] * 3, "fp16", "bf16")]
+
+
+@pytest.mark.parametrize("block,count,coeffs,chain,wdt", SMALL)
+def test_small_blocks_in_one_launch(block, count, coeffs, chain, wdt):
+    (w, _), (g, _), (m, _) = (make((count, *block), "odd" if block[1] % 2 else None, dt, 60 + i, s) for i, (dt, s) in enumerate(
+        ((TYPES[wdt], 0.05), (torch.bfloat16, 1.0), (torch.float32, 0.2))))
+    old = [t.double().cpu() for t in (w, g)]
+    hp = {} if coeffs is None else {"coeffs": coeffs}
+    nsm.muon_profile_begin()
+    status = torch.full((count,), -1, dtype=torch.int32, device="cuda")
+    nsm.muon_step_blocks([w], [g], [m], [None], status=status, compute_dtype=chain, **hp)
+    assert "ns_block_kernel" in [r["kernel"] for r in nsm.muon_profile_end()]
+    assert status.tolist() == [0] * count
+    for e in range(count):
+        check_weights(w[e], old[0][e], 0.05 * old[1][e] + 0.95 * m[e].double().cpu(), block, chain, coeffs)
+
+
+def test_small_blocks_repeat_and_flag_what_is_not_finite():
+    """Bit for bit the same twice and in a graph; a NaN or a zero gradient stays with its block."""
+    shape, block = (512, 1024), (64, 1024)
+    outs = []
+    for mode in range(3):
+        w, g, m = (make(shape, None, dt, 70 + i, s)[0] for i, (dt, s) in enumerate(
+            ((torch.bfloat16, 0.05), (torch.bfloat16, 1.0), (torch.float32, 0.2))))
+        g[70, 5] = float("nan")
+        g[128:192], m[128:192] = 0, 0
+        w0 = w.clone()
+        step = nsm.MuonStep([w], [g], [m], blocks=[block])
+        if mode == 2:
+            graph = step.capture()
+            w.copy_(w0), m.copy_(make(shape, None, torch.float32, 72, 0.2)[0])
+            m[128:192] = 0
+            graph.replay()
+        else:
+            step()
+        assert step.status.tolist() == [0, 1, 0, 0, 0, 0, 0, 0]
+        assert not w[64:128].isfinite().any() and w[128:].isfinite().all() and w[:64].isfinite().all()
+        assert torch.equal(w[128:192], (0.998 * w0[128:192].float()).bfloat16())
+        outs.append([t.view(torch.int16 if t.element_size() == 2 else torch.int32) for t in (w, m)])
+    for o in outs[1:]:
+        assert torch.equal(o[0], outs[0][0]) and torch.equal(o[1], outs[0][1])
+
+
+def test_more_small_blocks_than_one_launch_takes():
+    w, g, m = (make((600, 8, 256), None, dt, 80 + i, s)[0] for i, (dt, s) in enumerate(
+        ((torch.bfloat16, 0.05), (torch.bfloat16, 1.0), (torch.float32, 0.2))))
+    w2, m2 = w.clone(), m.clone()
+    lo = nsm.muon_blocks_workspace_min([w], [g], [m], [None])
+    nsm.muon_step_blocks([w], [g], [m], [None])
+    nsm.muon_step_blocks([w2], [g], [m2], [None], workspace=torch.empty(20 * lo, dtype=torch.uint8, device="cuda"))
+    assert torch.equal(w, w2) and torch.equal(m, m2)
