@@ -40,10 +40,12 @@
 // accumulator, a bias that grows with the length of the sum (relative error
 // 1.3e-6 at 1024 tokens, 4.9e-6 at 4096, 1.9e-5 at 16384).  Where the result is
 // stored in fp32 a tile is therefore summed in runs of 512 tokens, each in a
-// fresh accumulator (two in TMEM), and 16 epilogue warps add the runs in
-// registers with round-to-nearest, 64 sums a thread, while the next run's MMAs
-// go on: 6.5e-7 at every length (3.5e-7 with runs of 256, which cost 6 % more;
-// a plain fp32 product 5.6e-7 at 1024).
+// fresh accumulator (two in TMEM), and the epilogue warps add the runs in
+// registers with round-to-nearest, 128 sums a thread, while the next run's MMAs
+// go on: 6.5e-7 at every length (a plain fp32 product 5.6e-7 at 1024 tokens), at
+// 270 us where the 16-bit result takes 240 (8192 rows, 8 experts of
+// 2048 x 7168).  Sixteen epilogue warps of 64 sums leave room for five stages
+// only: 311 us.
 //
 // Waits are bounded as in the other product kernels.
 #include <algorithm>
@@ -56,22 +58,19 @@ namespace muon {
 namespace tc {
 namespace expk {
 
-// per kernel: epilogue warps, threads (producer, MMA, epilogue and, for weight
-// gradients, the zeroing warp) and ring stages
-constexpr int epi_warps(bool out32) { return out32 ? 16 : NUM_EPI_WARPS; }
-constexpr int threads_of(bool wg, bool out32) { return 64 + 32 * epi_warps(out32) + (wg ? 32 : 0); }
-constexpr int stages_of(bool out32) { return out32 ? 5 : 6; }
+constexpr int NSTAGES = 6;
+constexpr int EPI = NUM_EPI_WARPS;
+// producer, MMA, epilogue and, for weight gradients, the zeroing warp
+constexpr int threads_of(bool wg) { return 64 + 32 * EPI + (wg ? 32 : 0); }
 constexpr int FOLD_KB = 8;                        // k-blocks of a run of an fp32 weight gradient: 512 tokens
 constexpr int HALF_BYTES = 128 * BK * 2;          // one operand of a stage in one CTA: 16 KB
 constexpr int STAGE2 = 2 * HALF_BYTES;
 constexpr int BOX_BYTES = STAGE_TILE_BYTES;       // one staging box per epilogue warp
 constexpr int TABLE_INTS = 3 * kMaxExperts + 8;   // segment starts, lengths, first tiles
 constexpr int BAR_BYTES = 256;
-constexpr int smem_of(bool out32) {
-  return stages_of(out32) * STAGE2 + epi_warps(out32) * BOX_BYTES + TABLE_INTS * 4 + BAR_BYTES + 1024;
-}
-static_assert(smem_of(false) <= 232448 && smem_of(true) <= 232448, "shared memory of one CTA");
-static_assert((3 * stages_of(false) + 5) * 8 + 8 <= BAR_BYTES, "barrier area");
+constexpr int SMEM = NSTAGES * STAGE2 + EPI * BOX_BYTES + TABLE_INTS * 4 + BAR_BYTES + 1024;
+static_assert(SMEM <= 232448, "shared memory of one CTA");
+static_assert((3 * NSTAGES + 5) * 8 + 8 <= BAR_BYTES, "barrier area");
 
 struct EParams {
   const int* offsets;
@@ -171,12 +170,11 @@ __device__ __forceinline__ ETile find_tile(const EParams& p, const Table& tb, Cu
 }
 
 template <int KIND, int IN_FMT, bool OUT32>
-__global__ void __launch_bounds__(threads_of(KIND == kWeightGrad, OUT32), 1)
+__global__ void __launch_bounds__(threads_of(KIND == kWeightGrad), 1)
 expert_kernel(const __grid_constant__ EMaps maps, const __grid_constant__ EParams p) {
   static_assert(KIND == kWeightGrad || !OUT32, "fp32 results: weight gradients only");
   constexpr bool WG = KIND == kWeightGrad;
   constexpr bool A_MN = KIND != kForward;   // A is read along its columns
-  constexpr int NSTAGES = stages_of(OUT32), EPI = epi_warps(OUT32);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* staging = smem + NSTAGES * STAGE2;
@@ -415,7 +413,8 @@ expert_kernel(const __grid_constant__ EMaps maps, const __grid_constant__ EParam
   } else if (OUT32) {
     // ---------------------------------------------------------------- fp32 epilogue (both CTAs): runs added in registers
     const int q = warp & 3;         // TMEM lane quarter
-    const int c0 = (warp - 2) >> 2 << 6;  // this warp's 64 columns
+    constexpr int COLS = 128;       // columns of a warp
+    const int c0 = ((warp - 2) >> 2) * COLS;
     uint8_t* S = staging + (warp - 2) * BOX_BYTES;
     const uint32_t s0 = smem_u32(S);
     int it = 0;
@@ -427,9 +426,9 @@ expert_kernel(const __grid_constant__ EMaps maps, const __grid_constant__ EParam
       const int gj = tl.c * 256 + c0;
       const bool mine = fi < p.F && gj < p.C;
       const int runs = max(1, (tl.len + FOLD_KB * BK - 1) / (FOLD_KB * BK));
-      float sum[64];
+      float sum[COLS];
 #pragma unroll
-      for (int j = 0; j < 64; ++j) sum[j] = 0.f;
+      for (int j = 0; j < COLS; ++j) sum[j] = 0.f;
       for (int run = 0; run < runs; ++run, ++it) {
         const int acc = it & 1;
         const uint32_t aph = (uint32_t)(it >> 1) & 1u;
@@ -440,7 +439,7 @@ expert_kernel(const __grid_constant__ EMaps maps, const __grid_constant__ EParam
         if (mine && tl.len > 0) {
           const uint32_t tbase = tmem_base + (uint32_t)(acc * BN + c0) + ((uint32_t)(q * 32) << 16);
 #pragma unroll
-          for (int h = 0; h < 4; ++h) {
+          for (int h = 0; h < COLS / 16; ++h) {
             uint32_t r[16];
             tmem_ld16(tbase + h * 16, r);
 #pragma unroll
@@ -457,7 +456,7 @@ expert_kernel(const __grid_constant__ EMaps maps, const __grid_constant__ EParam
       if (!ok || !mine) continue;
       // boxes of 16 columns
 #pragma unroll
-      for (int h = 0; h < 4; ++h) {
+      for (int h = 0; h < COLS / 16; ++h) {
         if (gj + h * 16 >= p.C) break;
         if (lane == 0) bulk_wait_read0();
         __syncwarp();
@@ -614,15 +613,14 @@ static int launch(const EMaps& maps, const EParams& p, long long tiles, cudaStre
   attr[0].val.clusterDim.x = 2;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
-  constexpr int smem = smem_of(OUT32);
-  cfg.blockDim = dim3(threads_of(KIND == kWeightGrad, OUT32));
-  cfg.dynamicSmemBytes = smem;
+  cfg.blockDim = dim3(threads_of(KIND == kWeightGrad));
+  cfg.dynamicSmemBytes = SMEM;
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   int max_pairs = max_pairs_of[dev].load(std::memory_order_acquire);
   if (max_pairs <= 0) {
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
     if (e != cudaSuccess) return (int)e;
     cfg.gridDim = dim3(2 * (num_sms() / 2));
     int n = 0;
