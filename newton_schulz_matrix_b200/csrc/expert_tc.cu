@@ -393,14 +393,11 @@ expert_kernel(const __grid_constant__ EMaps maps, const __grid_constant__ EParam
         if (!__shfl_sync(0xffffffffu, ok, 0)) break;
         __syncwarp();
         seen ^= 1u << s;
-        // rows [rem, rem rounded up to 16) of the four 64-column boxes, 128 bytes each
-        uint8_t* sm = smem + s * STAGE2;
+        // rows [rem, rem rounded up to 16) of the four 64-column boxes: 128 bytes
+        // each, so the 32 lanes clear one row of all four per step
+        uint8_t* sm = smem + s * STAGE2 + (lane >> 3) * (BK * 128) + (lane & 7) * 16;
         const int rem = tl.len & (BK - 1), upto = (rem + 15) & ~15;
-        const int per = (upto - rem) * 8;  // 16-byte pieces per box
-        for (int i = lane; i < per * 4; i += 32) {
-          const int box = i / per, k = i - box * per;
-          *reinterpret_cast<uint4*>(sm + box * (BK * 128) + (rem + (k >> 3)) * 128 + (k & 7) * 16) = make_uint4(0, 0, 0, 0);
-        }
+        for (int r = rem; r < upto; ++r) *reinterpret_cast<uint4*>(sm + r * 128) = make_uint4(0, 0, 0, 0);
         fence_async_smem();  // the MMA reads these rows through the async proxy
         __syncwarp();
         if (lane == 0) {
