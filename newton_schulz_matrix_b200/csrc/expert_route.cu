@@ -28,22 +28,26 @@ namespace {
 // ----------------------------------------------------------------------------
 // A block ranks a run of consecutive assignments in two passes over them, its
 // 32 warps taking consecutive pieces: pass 1 counts each warp's keys (lanes of
-// equal key found with match_any, one add per distinct key), a prefix over the
+// equal key found by votes, one add per distinct key), a prefix over the
 // warps and the experts turns the counts into first positions, and pass 2
 // walks the same pieces again and hands positions out in order, so equal keys
 // keep their order and no atomic decides a position.  A warp loads kKeys groups
 // of 32 keys at once and, where its piece is no longer, keeps them for pass 2:
 // one group at a time waits for memory at every group (131072 x 8 ids to 64
-// experts: 26.3 us, 24.6 with groups of eight).
+// experts: 26.3 us, 24.6 with groups of eight; 18 with votes in place of
+// match_any and the early start below).
 //
-// Up to kSortOneBlock assignments run as one block and one launch; beyond, a
-// first launch counts the keys of up to one run per SM, and every block of the
-// second launch sums the counts of the runs before its own.
+// Up to kSortOneBlock assignments run as one block and one launch (2048 to 64
+// experts 6.6 us, two launches 6.9; 4096: 9.0 and 6.8); beyond, a first launch counts the keys of up
+// to one run per SM, and every block of the second launch sums the counts of the
+// runs before its own.  The second launch counts its own warps' keys while the
+// first still runs (programmatic dependent launch).
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
-constexpr int kSortOneBlock = 8192;
-constexpr int kSortMinRun = 4096;
+constexpr int kSortOneBlock = 2048;
+constexpr int kSortMinRun = 1024;
 constexpr int kKeys = 8;
+constexpr int kSortOwnSm = 120 * 1024;
 
 __device__ __forceinline__ int key_of(const SortArgs& a, int i) {
   const long long at = a.ld == a.topk ? (long long)i : (long long)(i / a.topk) * a.ld + i % a.topk;
@@ -51,9 +55,21 @@ __device__ __forceinline__ int key_of(const SortArgs& a, int i) {
   return id >= 0 && id < a.experts ? (int)id : a.experts;  // bucket `experts`: no expert
 }
 
+// The lanes of this warp that hold the same key, by one vote per bit of the keys.
+__device__ __forceinline__ unsigned lanes_of(int key, int bits) {
+  unsigned same = 0xffffffffu;
+  for (int i = 0; i < bits; ++i) {
+    const bool on = (key >> i) & 1;
+    const unsigned votes = __ballot_sync(0xffffffffu, on);
+    same &= on ? votes : ~votes;
+  }
+  return same;
+}
+
 __global__ void __launch_bounds__(kSortThreads)
 expert_count_kernel(const SortArgs a, int n, int run, int* __restrict__ counts) {
   extern __shared__ int hist[];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   for (int e = threadIdx.x; e <= a.experts; e += kSortThreads) hist[e] = 0;
   __syncthreads();
   const int first = blockIdx.x * run, last = min(n, first + run);
@@ -91,6 +107,7 @@ expert_rank_kernel(const SortArgs a, int n, int run, int warps, const int* __res
   const int piece = ((last - first + warps - 1) / warps + 31) / 32 * 32;
   const int p0 = first + warp * piece, p1 = warp < warps ? min(last, p0 + piece) : p0;
   int* mine = hist + warp * buckets;
+  const int bits = 32 - __clz(buckets);  // of keys 0 .. buckets (no assignment)
   int key[kKeys];
   auto load = [&](int i0) {
 #pragma unroll
@@ -104,12 +121,13 @@ expert_rank_kernel(const SortArgs a, int n, int run, int warps, const int* __res
 #pragma unroll
     for (int q = 0; q < kKeys; ++q) {
       if (i0 + q * 32 >= p1) break;
-      const unsigned same = __match_any_sync(0xffffffffu, key[q]);
+      const unsigned same = lanes_of(key[q], bits);
       if (key[q] < buckets && lane == __ffs(same) - 1) mine[key[q]] += __popc(same);
       __syncwarp();
     }
   }
   if (gridDim.x > 1) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // the counts are complete
     // groups of threads share a bucket's column of counts; integer sums, so
     // their order does not matter
     const int groups = max(1, kSortThreads / buckets), g = (int)threadIdx.x / buckets;
@@ -175,7 +193,7 @@ expert_rank_kernel(const SortArgs a, int n, int run, int warps, const int* __res
     for (int q = 0; q < kKeys; ++q) {
       if (i0 + q * 32 >= p1) break;
       const int i = i0 + q * 32 + lane;
-      const unsigned same = __match_any_sync(0xffffffffu, key[q]);
+      const unsigned same = lanes_of(key[q], bits);
       const int leader = __ffs(same) - 1;
       int at = 0;
       if (key[q] < buckets && lane == leader) {
@@ -462,22 +480,38 @@ size_t expert_sort_ws_bytes(int tokens, int topk, int experts) {
 
 int launch_expert_sort(const SortArgs& a, int* ws, cudaStream_t s) {
   const SortPlan p = sort_plan(a.tokens, a.topk);
-  const size_t smem = (size_t)(p.warps + 2) * (a.experts + 1) * sizeof(int);
+  // more than half an SM's shared memory where there is a block per SM: blocks
+  // that start early would otherwise pair up on the first SMs that have room
+  // (131072 x 8 to 64 experts: 27 us, 19 without the early start, 18 so)
+  size_t smem = (size_t)(p.warps + 2) * (a.experts + 1) * sizeof(int);
+  if (p.blocks > 1) smem = std::max(smem, (size_t)kSortOwnSm);
   if (smem > 48 * 1024) {
     static std::atomic<int> opted[kMaxDevices];
     const int dev = current_device();
     if (dev < 0) return (int)cudaErrorInvalidDevice;
     if (!opted[dev].load(std::memory_order_acquire)) {
-      const int most = (kSortWarps + 2) * (kMaxExperts + 1) * (int)sizeof(int);
+      const int most = std::max((kSortWarps + 2) * (kMaxExperts + 1) * (int)sizeof(int), kSortOwnSm);
       const cudaError_t e = cudaFuncSetAttribute(expert_rank_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
       if (e != cudaSuccess) return (int)e;
       opted[dev].store(1, std::memory_order_release);
     }
   }
-  if (p.blocks > 1)
+  if (p.blocks > 1) {
     expert_count_kernel<<<p.blocks, kSortThreads, (a.experts + 1) * sizeof(int), s>>>(a, p.n, p.run, ws);
-  expert_rank_kernel<<<p.blocks, kSortThreads, smem, s>>>(a, p.n, p.run, p.warps, ws);
-  return (int)cudaGetLastError();
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return (int)e;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3(p.blocks);
+  cfg.blockDim = dim3(kSortThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = p.blocks > 1 ? 1 : 0;
+  return (int)cudaLaunchKernelEx(&cfg, expert_rank_kernel, a, p.n, p.run, p.warps, (const int*)ws);
 }
 
 int launch_expert_gather(const RouteArgs& a, cudaStream_t s) {
