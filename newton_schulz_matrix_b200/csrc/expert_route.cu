@@ -322,9 +322,12 @@ __device__ __forceinline__ Taken taken(const RouteArgs& a, long long t, int j0) 
 }
 
 // The rows are added in the order of the assignments; fp32 sum, rounded once.
-// A thread has U steps of columns in flight: one of 16 bytes, four of one element.
-template <typename T, int N, int U>
-__global__ void __launch_bounds__(512)
+// A thread has U steps of columns in flight: one of 16 bytes (two take the
+// registers of other warps, which hide more), four of one element.
+// MORE: more than kGroup assignments a token (they are then looked up again at
+// every step; kept apart, since the two loops together spill).
+template <typename T, int N, int U, bool MORE>
+__global__ void __launch_bounds__(256)
 expert_combine_kernel(const RouteArgs a, int units, int wpt) {
   using P = Pack<T, N>;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -360,7 +363,10 @@ expert_combine_kernel(const RouteArgs a, int units, int wpt) {
         }
     };
     add(head);
-    for (int j0 = kGroup; j0 < a.topk; j0 += kGroup) add(taken(a, t, j0));
+    if constexpr (MORE) {
+#pragma unroll 1
+      for (int j0 = kGroup; j0 < a.topk; j0 += kGroup) add(taken(a, t, j0));
+    }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       if (c + u * next >= units) break;
@@ -374,7 +380,7 @@ expert_combine_kernel(const RouteArgs a, int units, int wpt) {
 // dy is read once per kGroup assignments, each row of ys once, and every row
 // of dys is written once; the dot products go through a fixed tree (a lane's
 // columns, lanes, then the token's warps in order).
-template <typename T, int N>
+template <typename T, int N, int U>
 __global__ void __launch_bounds__(512)
 expert_combine_backward_kernel(const RouteArgs a, int units, int wpt) {
   using P = Pack<T, N>;
@@ -392,28 +398,38 @@ expert_combine_backward_kernel(const RouteArgs a, int units, int wpt) {
     for (int q = 0; q < kGroup; ++q) dot[q] = 0.f;
     if (live) {
       const Taken k = taken(a, t, j0);
-      for (int c = sub * 32 + lane; c < units; c += 32 * wpt) {
-        float g[N];
-        reinterpret_cast<const P*>(dy)[c].get(g);
-        P v[kGroup];
-        if (dots) {
+      const int next = 32 * wpt;
+      for (int c = sub * 32 + lane; c < units; c += next * U) {
+        P d[U], v[U][kGroup];
 #pragma unroll
-          for (int q = 0; q < kGroup; ++q)
-            if (k.row[q] >= 0) v[q] = reinterpret_cast<const P*>(ys + (long long)k.row[q] * a.ld_row)[c];
+        for (int u = 0; u < U; ++u) {
+          if (c + u * next >= units) break;
+          d[u] = reinterpret_cast<const P*>(dy)[c + u * next];
+          if (dots) {
+#pragma unroll
+            for (int q = 0; q < kGroup; ++q)
+              if (k.row[q] >= 0) v[u][q] = reinterpret_cast<const P*>(ys + (long long)k.row[q] * a.ld_row)[c + u * next];
+          }
         }
 #pragma unroll
-        for (int q = 0; q < kGroup; ++q) {
-          if (k.row[q] < 0) continue;
-          float f[N];
+        for (int u = 0; u < U; ++u) {
+          if (c + u * next >= units) break;
+          float g[N];
+          d[u].get(g);
 #pragma unroll
-          for (int i = 0; i < N; ++i) f[i] = k.w[q] * g[i];
-          P out;
-          out.set(f);
-          reinterpret_cast<P*>(dys + (long long)k.row[q] * a.ld_out_row)[c] = out;
-          if (dots) {
-            v[q].get(f);
+          for (int q = 0; q < kGroup; ++q) {
+            if (k.row[q] < 0) continue;
+            float f[N];
 #pragma unroll
-            for (int i = 0; i < N; ++i) dot[q] = fmaf(g[i], f[i], dot[q]);
+            for (int i = 0; i < N; ++i) f[i] = k.w[q] * g[i];
+            P out;
+            out.set(f);
+            reinterpret_cast<P*>(dys + (long long)k.row[q] * a.ld_out_row)[c + u * next] = out;
+            if (dots) {
+              v[u][q].get(f);
+#pragma unroll
+              for (int i = 0; i < N; ++i) dot[q] = fmaf(g[i], f[i], dot[q]);
+            }
           }
         }
       }
@@ -539,12 +555,13 @@ int launch_expert_combine(const RouteArgs& a, cudaStream_t s) {
   const int es = dtype_size(a.dtype);
   const bool vec = on16(a.by_row, a.ld_row, es) && on16(a.out_token, a.ld_out_token, es) && (long long)a.cols * es % 16 == 0;
   return with_type(a.dtype, vec, [&](auto type, auto n) {
-    const int units = a.cols / n, wpt = warps_per_token(a.tokens, units);
-    const int warps = std::max(8, wpt);
-    dim3 grid((unsigned)(((long long)a.tokens * wpt + warps - 1) / warps));
+    using T = decltype(type);
     constexpr int N = decltype(n)::value, U = N == 1 ? 4 : 1;
+    const int units = a.cols / N, wpt = std::min(8, warps_per_token(a.tokens, units));
+    dim3 grid((unsigned)(((long long)a.tokens * wpt + 7) / 8));
     grid.y = column_blocks(grid.x, units, 32 * wpt * U);
-    expert_combine_kernel<decltype(type), N, U><<<grid, 32 * warps, 0, s>>>(a, units, wpt);
+    if (a.topk <= kGroup) expert_combine_kernel<T, N, U, false><<<grid, 256, 0, s>>>(a, units, wpt);
+    else expert_combine_kernel<T, N, 1, true><<<grid, 256, 0, s>>>(a, units, wpt);
     return (int)cudaGetLastError();
   });
 }
@@ -558,7 +575,8 @@ int launch_expert_combine_backward(const RouteArgs& a, cudaStream_t s) {
     const int units = a.cols / n, wpt = warps_per_token(a.tokens, units);
     const int warps = std::max(8, wpt);
     const unsigned grid = (unsigned)(((long long)a.tokens * wpt + warps - 1) / warps);
-    expert_combine_backward_kernel<decltype(type), decltype(n)::value><<<grid, 32 * warps, 0, s>>>(a, units, wpt);
+    constexpr int N = decltype(n)::value, U = N == 1 ? 4 : 2;
+    expert_combine_backward_kernel<decltype(type), N, U><<<grid, 32 * warps, 0, s>>>(a, units, wpt);
     return (int)cudaGetLastError();
   });
 }
