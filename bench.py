@@ -82,9 +82,10 @@ def parse_args():
     p.add_argument("--sharded", action="store_true",
                    help="strong scaling: shard one workload across the ranks (ownership by NS FLOPs, owner "
                         "broadcast of the updated weights) instead of one full workload per rank")
-    p.add_argument("--report", choices=["stress", "parity"], default=None,
+    p.add_argument("--report", choices=["stress", "parity", "experts"], default=None,
                    help="stress: the ill-conditioned sweep (one JSON line per (n, alpha) point); parity: errors "
-                        "against the fp64 oracle on sampled matrices of each workload, every form")
+                        "against the fp64 oracle on sampled matrices of each workload, every form; experts: "
+                        "the expert layer's operators and the block step, one JSON line each")
     return p.parse_args()
 
 
@@ -469,6 +470,71 @@ def run_parity_report(args):
             torch.cuda.empty_cache()
 
 
+def run_experts_report(args):
+    """One training step of the MoE layer set's expert layer (64 experts, 16384
+    tokens to 6 of them, 2048 wide, 1408 hidden): routing, products, their
+    gradients and the block step on the fused gate and up, and the block step on
+    64 attention heads of 128 x 2048.  One JSON line per operator: device time,
+    its algorithmic bytes and FLOPs per second, and the share of the peaks."""
+    import newton_schulz_matrix_b200 as nsm
+    dev = torch.device("cuda", 0)
+    pk, source = load_peaks()
+    g = torch.Generator(device=dev).manual_seed(0)
+    tokens, topk, experts, width, hidden = 16384, 6, 64, 2048, 1408
+    rows = tokens * topk
+
+    def randn(*shape, std=1.0, dtype=torch.bfloat16):
+        return (torch.randn(*shape, generator=g, device=dev) * std).to(dtype)
+
+    ids = (torch.randn(tokens, experts, generator=g, device=dev) + 0.5 * torch.randn(experts, generator=g, device=dev)
+           ).topk(topk, dim=1).indices
+    x, probs = randn(tokens, width), torch.softmax(randn(tokens, topk, dtype=torch.float32), dim=1)
+    w1, w2 = randn(experts, 2 * hidden, width, std=0.02), randn(experts, width, hidden, std=0.02)
+    m1 = torch.zeros(experts, 2 * hidden, width, device=dev)
+    offsets, slot, _ = nsm.muon_expert_sort(ids, experts)
+    xs = nsm.muon_expert_gather(x, slot)
+    h, a = randn(rows, 2 * hidden), randn(rows, hidden)
+    o = nsm.muon_expert_product(a, w2, offsets)
+    dw = nsm.muon_expert_weight_grad(h, xs, offsets)
+    blocks = [(hidden, width)]
+    step = nsm.MuonStep([w1], [dw], [m1], blocks=blocks)
+    expert_step = nsm.ExpertMuonStep([w1], [m1], blocks=blocks)
+    heads = [randn(2048, 2048, std=0.02), randn(2048, 2048), torch.zeros(2048, 2048, device=dev)]
+    head_step = nsm.MuonStep(*[[t] for t in heads], blocks=[(128, 2048)])
+    ns = experts * 2 * nsm.muon_ns_flops(hidden, width)
+    es, fl = 2, 2.0 * rows * width
+    cases = [
+        ("muon_expert_sort", lambda: nsm.muon_expert_sort(ids, experts), 16.0 * rows, 0.0),
+        ("muon_expert_gather", lambda: nsm.muon_expert_gather(x, slot, out=xs), es * width * (tokens + rows), 0.0),
+        ("muon_expert_gather_backward", lambda: nsm.muon_expert_gather_backward(xs, slot), es * width * (tokens + rows), 0.0),
+        ("muon_expert_product", lambda: nsm.muon_expert_product(xs, w1, offsets, out=h), 0.0, fl * 2 * hidden),
+        ("muon_expert_input_grad", lambda: nsm.muon_expert_input_grad(h, w1, offsets, out=xs), 0.0, fl * 2 * hidden),
+        ("muon_expert_weight_grad", lambda: nsm.muon_expert_weight_grad(h, xs, offsets, out=dw), 0.0, fl * 2 * hidden),
+        ("muon_expert_combine", lambda: nsm.muon_expert_combine(o, slot, probs), es * width * (tokens + rows), 0.0),
+        ("muon_expert_combine_backward", lambda: nsm.muon_expert_combine_backward(x, o, slot, probs),
+         es * width * (tokens + 2 * rows), 0.0),
+        ("MuonStep on gate and up blocks", step, 0.0, ns),
+        ("ExpertMuonStep (weight gradients and step)", lambda: expert_step([(h, xs, offsets)]), 0.0, ns + fl * 2 * hidden),
+        ("MuonStep on 16 heads", head_step, 0.0, 16 * nsm.muon_ns_flops(128, 2048)),
+    ]
+    for name, call, nbytes, flops in cases:
+        for _ in range(max(3, args.warmup)):
+            call()
+        e0, e1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        e0.record()
+        for _ in range(args.steps):
+            call()
+        e1.record()
+        torch.cuda.synchronize()
+        us = e0.elapsed_time(e1) / args.steps * 1e3
+        line = {"report": "experts", "operator": name, "us": round(us, 2), "peaks": source}
+        if nbytes:
+            line.update(gb_s=round(nbytes / us / 1e3, 1), of_hbm=round(nbytes / us / 1e3 / pk["hbm_gbs"], 3))
+        if flops:
+            line.update(tflops=round(flops / us / 1e6, 1), of_bf16=round(flops / us / 1e6 / pk["bf16_tflops"], 3))
+        print(json.dumps(line), flush=True)
+
+
 def main():
     args = parse_args()
     if args.report == "stress":
@@ -476,6 +542,9 @@ def main():
         return
     if args.report == "parity":
         run_parity_report(args)
+        return
+    if args.report == "experts":
+        run_experts_report(args)
         return
     if args.impl == "reference":
         run_reference(args)

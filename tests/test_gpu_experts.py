@@ -215,17 +215,19 @@ def test_products_of_strided_weights(dtype):
     assert bool((out[:, :96] == 7).all()) and bool((out[:, :, :64] == 7).all())
 
 
+@pytest.mark.parametrize("scale", [1, 9])
 @pytest.mark.parametrize("dtype", [BF, HF, SF])
-def test_nan_stays_with_its_expert(dtype):
+def test_nan_stays_with_its_expert(dtype, scale):
     """Inf and NaN in one expert's rows reach no other expert's results, whatever tile they share."""
-    counts = [21, 9, 34, 100, 3]
+    counts = [21 * scale, 9 * scale, 34 * scale, 100 * scale, 3 * scale]
     offsets, xs, dys, w = product_case(15, counts, 128, 64, dtype, tail=0)
+    lo, hi = counts[0], counts[0] + counts[1]
     clean = [f(a, b, offsets) for f, a, b in ((nsm.muon_expert_product, xs, w), (nsm.muon_expert_input_grad, dys, w),
                                               (nsm.muon_expert_weight_grad, dys, xs))]
-    xs[21:30], dys[21:30] = float("nan"), float("inf")
+    xs[lo:hi], dys[lo:hi] = float("nan"), float("inf")
     dirty = [f(a, b, offsets) for f, a, b in ((nsm.muon_expert_product, xs, w), (nsm.muon_expert_input_grad, dys, w),
                                               (nsm.muon_expert_weight_grad, dys, xs))]
-    rest = torch.cat([torch.arange(21), torch.arange(30, 167)]).cuda()
+    rest = torch.cat([torch.arange(lo), torch.arange(hi, sum(counts))]).cuda()
     for a, b in zip(clean[:2], dirty[:2]):
         assert torch.equal(a[rest], b[rest])
     assert torch.equal(clean[2][[0, 2, 3, 4]], dirty[2][[0, 2, 3, 4]]) and not dirty[2][1].isfinite().any()
@@ -269,7 +271,7 @@ def test_weight_gradients_accumulate(dtype):
     assert torch.equal(out[1], base[1]) and not one[1].any()
 
 
-@pytest.mark.parametrize("rows,experts", [(1, 64), (8, 64), (200, 64), (3000, 300)])
+@pytest.mark.parametrize("rows,experts", [(1, 64), (8, 64), (200, 64), (3000, 300), (2000, 1024)])
 def test_products_of_many_experts_with_few_rows(rows, experts):
     g = gen(19)
     to = torch.randint(0, experts, (rows,), generator=g, device="cuda").sort().values
