@@ -220,9 +220,8 @@ MUON_API int muon_ns_batched_noalloc(void* const* X, int count, int rows, int co
  *            row; behind the last row, those that no expert takes, in order
  * Matrices are row-major with a row pitch ld >= cols in elements and any
  * alignment of their elements; rows that start on 16 bytes are moved faster,
- * and the 16-bit products need it for the tensor cores (base, pitch and expert
- * stride multiples of 16 bytes; others run on the CUDA cores).  Sorted rows that
- * no expert owns are neither read into a result nor written.  All sums are held
+ * and the 16-bit products' operands need it for the tensor cores (see there).
+ * Sorted rows that no expert owns are neither read into a result nor written.  All sums are held
  * in fp32 and rounded once, in an order that does not change from call to call.
  * Row counts and tokens * topk are at most 2^31 - 1, experts at most 1024.
  *
@@ -262,18 +261,30 @@ MUON_API int muon_expert_combine_backward(const void* dy, long long ld_dy, const
  *   muon_expert_weight_grad   dW[e]  = sum_p dys[p] xs[p]^T  over e's rows p
  * dW[e] (outer x inner at dw + e * stride_dw) has the operands' type or fp32; an
  * expert without rows gets zeros.  accumulate (fp32 dW only) adds to dW instead.
+ * 16-bit operands run on the tensor cores where base, pitch and expert stride are
+ * multiples of 16 bytes (and the stride is not 0).  Others are first copied into
+ * such rows in the workspace, where it holds muon_expert_workspace_size bytes;
+ * without it, where that is 0 (small products), and in fp32 the CUDA cores run.
  * status: one optional device word, zeroed by the call, MUON_STATUS_TIMEOUT when
  * a device-side wait gave up. */
+enum { MUON_EXPERT_PRODUCT = 0, MUON_EXPERT_INPUT_GRAD = 1, MUON_EXPERT_WEIGHT_GRAD = 2 };
+/* Workspace bytes with which the product `kind` of these operands runs on the
+ * tensor cores (a: xs or dys, b: w, or xs for the weight gradient); 0: none needed
+ * or none used.  Results do not depend on the workspace beyond the order of their
+ * fp32 sums. */
+MUON_API size_t muon_expert_workspace_size(int kind, const void* a, long long ld_a, const void* b, long long ld_b,
+                                           long long stride_b, int experts, long long rows, int inner, int outer,
+                                           int dtype);
 MUON_API int muon_expert_product(const void* xs, long long ld_xs, const void* w, long long ld_w, long long stride_w,
                                  const int* offsets, int experts, long long rows, int inner, int outer, int dtype,
-                                 void* y, long long ld_y, int* status, void* stream);
+                                 void* y, long long ld_y, void* ws, size_t ws_bytes, int* status, void* stream);
 MUON_API int muon_expert_input_grad(const void* dys, long long ld_dys, const void* w, long long ld_w, long long stride_w,
                                     const int* offsets, int experts, long long rows, int inner, int outer, int dtype,
-                                    void* dxs, long long ld_dxs, int* status, void* stream);
+                                    void* dxs, long long ld_dxs, void* ws, size_t ws_bytes, int* status, void* stream);
 MUON_API int muon_expert_weight_grad(const void* dys, long long ld_dys, const void* xs, long long ld_xs,
                                      const int* offsets, int experts, long long rows, int inner, int outer, int dtype,
                                      void* dw, long long ld_dw, long long stride_dw, int dw_dtype, int accumulate,
-                                     int* status, void* stream);
+                                     void* ws, size_t ws_bytes, int* status, void* stream);
 
 /* Algorithmic FLOPs of one orthogonalisation of a rows x cols matrix, every
  * product counted as 2 * rows * cols * inner [GramNS cost list]. */

@@ -43,6 +43,7 @@ EXPORTED_SYMBOLS = (
     "muon_ns_batched_noalloc", "muon_blocks_workspace_size", "muon_blocks_workspace_min", "muon_step_blocks",
     "muon_expert_sort_workspace_size", "muon_expert_sort", "muon_expert_gather", "muon_expert_combine",
     "muon_expert_combine_backward", "muon_expert_product", "muon_expert_input_grad", "muon_expert_weight_grad",
+    "muon_expert_workspace_size",
 )
 EXPERT_MAX = 1024
 NOALLOC_SCRATCH_BYTES = 64 << 20
@@ -131,9 +132,12 @@ def load_library() -> ctypes.CDLL:
     lib.muon_expert_gather.argtypes = [P, L, P, I, I, I, I, P, L, L, P]
     lib.muon_expert_combine.argtypes = [P, L, L, P, P, I, I, I, I, I, P, L, P]
     lib.muon_expert_combine_backward.argtypes = [P, L, P, L, L, P, P, I, I, I, I, I, P, L, P, P]
-    lib.muon_expert_product.argtypes = [P, L, P, L, L, P, I, L, I, I, I, P, L, P, P]
-    lib.muon_expert_input_grad.argtypes = [P, L, P, L, L, P, I, L, I, I, I, P, L, P, P]
-    lib.muon_expert_weight_grad.argtypes = [P, L, P, L, P, I, L, I, I, I, P, L, L, I, I, P, P]
+    S = ctypes.c_size_t
+    lib.muon_expert_workspace_size.argtypes = [I, P, L, P, L, L, I, L, I, I, I]
+    lib.muon_expert_workspace_size.restype = S
+    lib.muon_expert_product.argtypes = [P, L, P, L, L, P, I, L, I, I, I, P, L, P, S, P, P]
+    lib.muon_expert_input_grad.argtypes = [P, L, P, L, L, P, I, L, I, I, I, P, L, P, S, P, P]
+    lib.muon_expert_weight_grad.argtypes = [P, L, P, L, P, I, L, I, I, I, P, L, L, I, I, P, S, P, P]
     for name in ("muon_step_blocks", "muon_expert_sort", "muon_expert_gather", "muon_expert_combine",
                  "muon_expert_combine_backward", "muon_expert_product", "muon_expert_input_grad",
                  "muon_expert_weight_grad"):
@@ -867,6 +871,17 @@ def _status_arg(status, device: torch.device):
     return status.data_ptr()
 
 
+def _pack_space(kind: int, a, ld_a: int, b, ld_b: int, stride_b: int, experts: int, rows: int, inner: int, outer: int,
+                code: int):
+    """The workspace in which a product copies operands that TMA cannot address (None: it needs none)."""
+    if code == FP32 or not ((a.data_ptr() | b.data_ptr()) | ((ld_a | ld_b | stride_b) << 1)) & 15 and (
+            stride_b or kind == 2 or experts == 1):
+        return None
+    need = load_library().muon_expert_workspace_size(kind, a.data_ptr(), ld_a, b.data_ptr(), ld_b, stride_b, experts, rows,
+                                                     inner, outer, code)
+    return torch.empty(need, dtype=torch.uint8, device=a.device) if need else None
+
+
 def muon_expert_product(xs: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, *, out: torch.Tensor | None = None,
                         status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """Every expert's rows times its weights: out[p] = w[e] @ xs[p] for the rows
@@ -876,9 +891,9 @@ def muon_expert_product(xs: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor
     with contiguous rows and any other strides; ``offsets`` as from
     muon_expert_sort, read on the device.  Rows of ``out`` (rows, outer) that no
     expert owns keep their contents.  bf16 and fp16 run on the tensor cores
-    where bases and strides are multiples of 16 bytes; fp32, and what TMA cannot
-    address, on the CUDA cores.  ``status``: one int32 word for a device-side
-    timeout.
+    (operands whose bases and strides are no multiples of 16 bytes after a copy
+    into rows that are; small ones of that kind on the CUDA cores), fp32 on the
+    CUDA cores.  ``status``: one int32 word for a device-side timeout.
     """
     device, dtype, code, rows, width, ld = _lead(xs, "xs")
     experts = _offsets_arg(offsets, device)
@@ -891,9 +906,10 @@ def muon_expert_product(xs: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor
         return _elsewhere(device, stream, muon_expert_product, xs, w, offsets, out=out, status=status)
     if out is None:
         out = torch.empty(rows, outer, dtype=dtype, device=device)
+    ws = _pack_space(0, xs, ld, w, ld_w, stride_w, experts, rows, inner, outer, code)
     _raise(load_library().muon_expert_product(
         xs.data_ptr(), ld, w.data_ptr(), ld_w, stride_w, offsets.data_ptr(), experts, rows, inner, outer, code,
-        out.data_ptr(), ld_out, word, _raw_stream(device.index)), "muon_expert_product")
+        out.data_ptr(), ld_out, None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(), word, _raw_stream(device.index)), "muon_expert_product")
     return out
 
 
@@ -912,9 +928,10 @@ def muon_expert_input_grad(dys: torch.Tensor, w: torch.Tensor, offsets: torch.Te
         return _elsewhere(device, stream, muon_expert_input_grad, dys, w, offsets, out=out, status=status)
     if out is None:
         out = torch.empty(rows, inner, dtype=dtype, device=device)
+    ws = _pack_space(1, dys, ld, w, ld_w, stride_w, experts, rows, inner, outer, code)
     _raise(load_library().muon_expert_input_grad(
         dys.data_ptr(), ld, w.data_ptr(), ld_w, stride_w, offsets.data_ptr(), experts, rows, inner, outer, code,
-        out.data_ptr(), ld_out, word, _raw_stream(device.index)), "muon_expert_input_grad")
+        out.data_ptr(), ld_out, None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(), word, _raw_stream(device.index)), "muon_expert_input_grad")
     return out
 
 
@@ -951,9 +968,11 @@ def muon_expert_weight_grad(dys: torch.Tensor, xs: torch.Tensor, offsets: torch.
                           accumulate=accumulate, status=status)
     if out is None:
         out = torch.empty(experts, outer, inner, dtype=out_dtype, device=device)
+    ws = _pack_space(2, dys, ld_dys, xs, ld_xs, 0, experts, rows, inner, outer, code)
     _raise(load_library().muon_expert_weight_grad(
         dys.data_ptr(), ld_dys, xs.data_ptr(), ld_xs, offsets.data_ptr(), experts, rows, inner, outer, code,
-        out.data_ptr(), ld_out, stride_out, odt, int(accumulate), word,
+        out.data_ptr(), ld_out, stride_out, odt, int(accumulate), None if ws is None else ws.data_ptr(),
+        0 if ws is None else ws.numel(), word,
         _raw_stream(device.index)), "muon_expert_weight_grad")
     return out
 

@@ -55,6 +55,8 @@ struct ExpertDesc {
 };
 bool expert_tc_ok(const ExpertDesc& g);   // whether expert_tc takes it: 16-bit operands that TMA can address
 int expert_tc(const ExpertDesc& g, cudaStream_t s);     // tensor cores (expert_tc.cu)
+size_t expert_pack_bytes(const ExpertDesc& g);          // workspace with which expert_tc_packed takes it; 0: it does not
+int expert_tc_packed(const ExpertDesc& g, void* ws, cudaStream_t s);   // after copying operands into aligned rows
 int expert_simt(const ExpertDesc& g, cudaStream_t s);   // any type, alignment and pitch (expert_simt.cu)
 
 }  // namespace muon

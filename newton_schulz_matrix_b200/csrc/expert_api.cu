@@ -54,7 +54,7 @@ int check_product(const int* offsets, int experts, long long rows, int inner, in
   return MUON_OK;
 }
 
-int run_product(const ExpertDesc& g, cudaStream_t s) {
+int run_product(const ExpertDesc& g, void* ws, size_t ws_bytes, cudaStream_t s) {
   if (g.status != nullptr && (!element_aligned(g.status, MUON_FP32) || cudaMemsetAsync(g.status, 0, sizeof(int), s) != cudaSuccess))
     return MUON_ERR_INVALID;
   if (g.rows == 0 && (g.kind != kWeightGrad || g.accumulate)) return MUON_OK;
@@ -62,9 +62,12 @@ int run_product(const ExpertDesc& g, cudaStream_t s) {
   const double es = dtype_size(g.dtype);
   const double bytes = (double)g.rows * (g.inner + g.outer) * es +
                        (double)g.experts * g.inner * g.outer * (g.kind == kWeightGrad ? dtype_size(g.d_dtype) : es);
-  const bool tc = expert_tc_ok(g);
-  ProfScope ps(tc ? kProfExpertProduct : kProfExpertSimt, flops, bytes, s);
-  return (tc ? expert_tc(g, s) : expert_simt(g, s)) == 0 ? MUON_OK : MUON_ERR_CUDA;
+  const bool tc = g.rows > 0 && expert_tc_ok(g);
+  const size_t pack = g.rows > 0 ? expert_pack_bytes(g) : 0;
+  const bool packed = !tc && pack > 0 && ws != nullptr && ws_bytes >= pack;
+  ProfScope ps(tc || packed ? kProfExpertProduct : kProfExpertSimt, flops, bytes, s);
+  const int rc = tc ? expert_tc(g, s) : packed ? expert_tc_packed(g, ws, s) : expert_simt(g, s);
+  return rc == 0 ? MUON_OK : MUON_ERR_CUDA;
 }
 
 }  // namespace
@@ -149,21 +152,31 @@ int muon_expert_combine_backward(const void* dy, long long ld_dy, const void* ys
   return launch_expert_combine_backward(a, s) == 0 ? MUON_OK : MUON_ERR_CUDA;
 }
 
+size_t muon_expert_workspace_size(int kind, const void* a, long long ld_a, const void* b, long long ld_b,
+                                  long long stride_b, int experts, long long rows, int inner, int outer, int dtype) {
+  if (kind < MUON_EXPERT_PRODUCT || kind > MUON_EXPERT_WEIGHT_GRAD || experts <= 0 || experts > kMaxExperts || rows <= 0 ||
+      rows > kMaxRows || inner <= 0 || outer <= 0 || !dtype_ok(dtype))
+    return 0;
+  const ExpertDesc g{kind, nullptr, experts, rows, inner, outer, dtype, a, ld_a, b, ld_b, stride_b, nullptr, 0, 0, dtype, 0,
+                     nullptr};
+  return expert_pack_bytes(g);
+}
+
 int muon_expert_product(const void* xs, long long ld_xs, const void* w, long long ld_w, long long stride_w,
                         const int* offsets, int experts, long long rows, int inner, int outer, int dtype, void* y,
-                        long long ld_y, int* status, void* stream) {
+                        long long ld_y, void* ws, size_t ws_bytes, int* status, void* stream) {
   const int rc = check_product(offsets, experts, rows, inner, outer, dtype);
   if (rc != MUON_OK) return rc;
   if (rows > 0 && (!matrix_ok(xs, ld_xs, inner, dtype) || !matrix_ok(w, ld_w, inner, dtype) ||
                    !matrix_ok(y, ld_y, outer, dtype) || stride_w < 0))
     return MUON_ERR_INVALID;
   ExpertDesc g{kForward, offsets, experts, rows, inner, outer, dtype, xs, ld_xs, w, ld_w, stride_w, y, ld_y, 0, dtype, 0, status};
-  return run_product(g, reinterpret_cast<cudaStream_t>(stream));
+  return run_product(g, ws, ws_bytes, reinterpret_cast<cudaStream_t>(stream));
 }
 
 int muon_expert_input_grad(const void* dys, long long ld_dys, const void* w, long long ld_w, long long stride_w,
                            const int* offsets, int experts, long long rows, int inner, int outer, int dtype, void* dxs,
-                           long long ld_dxs, int* status, void* stream) {
+                           long long ld_dxs, void* ws, size_t ws_bytes, int* status, void* stream) {
   const int rc = check_product(offsets, experts, rows, inner, outer, dtype);
   if (rc != MUON_OK) return rc;
   if (rows > 0 && (!matrix_ok(dys, ld_dys, outer, dtype) || !matrix_ok(w, ld_w, inner, dtype) ||
@@ -171,12 +184,13 @@ int muon_expert_input_grad(const void* dys, long long ld_dys, const void* w, lon
     return MUON_ERR_INVALID;
   ExpertDesc g{kInputGrad, offsets, experts, rows, inner, outer, dtype, dys, ld_dys, w, ld_w, stride_w, dxs, ld_dxs, 0,
                dtype, 0, status};
-  return run_product(g, reinterpret_cast<cudaStream_t>(stream));
+  return run_product(g, ws, ws_bytes, reinterpret_cast<cudaStream_t>(stream));
 }
 
 int muon_expert_weight_grad(const void* dys, long long ld_dys, const void* xs, long long ld_xs, const int* offsets,
                             int experts, long long rows, int inner, int outer, int dtype, void* dw, long long ld_dw,
-                            long long stride_dw, int dw_dtype, int accumulate, int* status, void* stream) {
+                            long long stride_dw, int dw_dtype, int accumulate, void* ws, size_t ws_bytes, int* status,
+                            void* stream) {
   const int rc = check_product(offsets, experts, rows, inner, outer, dtype);
   if (rc != MUON_OK) return rc;
   // the result's type: the operands' or fp32; sums over several calls are held in fp32
@@ -186,7 +200,7 @@ int muon_expert_weight_grad(const void* dys, long long ld_dys, const void* xs, l
   if (rows > 0 && (!matrix_ok(dys, ld_dys, outer, dtype) || !matrix_ok(xs, ld_xs, inner, dtype))) return MUON_ERR_INVALID;
   ExpertDesc g{kWeightGrad, offsets, experts, rows, inner, outer, dtype, dys, ld_dys, xs, ld_xs, 0, dw, ld_dw, stride_dw,
                dw_dtype, accumulate ? 1 : 0, status};
-  return run_product(g, reinterpret_cast<cudaStream_t>(stream));
+  return run_product(g, ws, ws_bytes, reinterpret_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

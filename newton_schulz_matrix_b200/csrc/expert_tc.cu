@@ -63,6 +63,7 @@ constexpr int NSTAGES = 6;
 constexpr int EPI = NUM_EPI_WARPS;
 // producer, MMA, epilogue and, for weight gradients, the zeroing warp
 constexpr int threads_of(bool wg) { return 64 + 32 * EPI + (wg ? 32 : 0); }
+constexpr double PACK_FLOPS = 2e8;                // least product whose operands are copied into aligned rows
 constexpr int SINGLE_TOKENS = 48;                 // tokens per expert up to which single CTAs run
 constexpr int FOLD_KB = 8;                        // k-blocks of a run of an fp32 weight gradient: 512 tokens
 constexpr int HALF_BYTES = 128 * BK * 2;          // one operand of a stage in one CTA: 16 KB
@@ -81,8 +82,8 @@ struct EParams {
   int C;                 // columns of D (weight grad): inner
   int K;                 // contraction of forward (inner) and input grad (outer)
   int tiles_f, tiles_c;
-  void* D; long long ldd;
-  int d_dtype;
+  void* D; long long ldd, stride_d;
+  int d_vec;             // 1: D's rows start on 16 bytes (TMA and 16-byte stores); 0: element by element
   int accumulate;
   int* err;
   long long timeout_ns;
@@ -487,6 +488,18 @@ expert_kernel(const __grid_constant__ EMaps maps, const __grid_constant__ EParam
         for (int k = 0; k < 4; ++k)
           *reinterpret_cast<float4*>(S + sw64(lane, k)) =
               make_float4(sum[h * 16 + k * 4], sum[h * 16 + k * 4 + 1], sum[h * 16 + k * 4 + 2], sum[h * 16 + k * 4 + 3]);
+        if (!p.d_vec) {
+          __syncwarp();
+          const int col = gj + h * 16 + (lane & 15);
+          float* d = reinterpret_cast<float*>(p.D) + tl.e * p.stride_d + col;
+          for (int r = lane >> 4; r < min(32, p.F - fi); r += 2) {
+            if (col >= p.C) continue;
+            const float v = *reinterpret_cast<const float*>(S + sw64(r, (lane & 15) >> 2) + (lane & 3) * 4);
+            float* at = d + (fi + r) * p.ldd;
+            *at = p.accumulate ? *at + v : v;
+          }
+          continue;
+        }
         fence_async_smem();
         __syncwarp();
         if (lane == 0) {
@@ -546,7 +559,13 @@ expert_kernel(const __grid_constant__ EMaps maps, const __grid_constant__ EParam
         __syncwarp();
 #pragma unroll
         for (int k = 0; k < 4; ++k) *reinterpret_cast<uint4*>(S + sw64(lane, k)) = dq[k];
-        if (WG) {
+        if (WG && !p.d_vec) {
+          __syncwarp();
+          const int col = tl.c * 256 + c * 32 + lane;
+          uint16_t* d = reinterpret_cast<uint16_t*>(p.D) + tl.e * p.stride_d + col;
+          for (int k = 0; k < min(32, p.F - fi); ++k)
+            if (col < p.C) d[(fi + k) * p.ldd] = *reinterpret_cast<const uint16_t*>(S + sw64(k, lane >> 3) + (lane & 7) * 2);
+        } else if (WG) {
           fence_async_smem();
           __syncwarp();
           if (lane == 0) {
@@ -572,7 +591,13 @@ expert_kernel(const __grid_constant__ EMaps maps, const __grid_constant__ EParam
                          : "memory");
           const int valid = tl.tokens - c * 32;         // tokens of this box that are the expert's
           const int row = tl.lo + tl.t0 + c * 32;
-          if (valid >= 32) {
+          if (!p.d_vec) {
+            __syncwarp();
+            uint16_t* d = reinterpret_cast<uint16_t*>(p.D) + fi + lane;
+            for (int k = 0; k < min(32, valid); ++k)
+              if (fi + lane < p.F)
+                d[(row + k) * p.ldd] = *reinterpret_cast<const uint16_t*>(S + sw64(k, lane >> 3) + (lane & 7) * 2);
+          } else if (valid >= 32) {
             fence_async_smem();
             __syncwarp();
             if (lane == 0) {
@@ -664,6 +689,23 @@ static bool on16(const void* p, long long ld, int es) {
   return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && ld * es % 16 == 0;
 }
 
+// Rows of any alignment (per > 0: matrices of `per` rows, `stride` apart) into
+// rows of `units` 16-byte units, zeros behind the columns.
+__global__ void __launch_bounds__(256)
+expert_pack_kernel(const uint16_t* __restrict__ src, long long ld, long long stride, int per, long long rows, int cols,
+                   int units, uint4* __restrict__ dst) {
+  for (long long r = (long long)blockIdx.x * blockDim.y + threadIdx.y; r < rows; r += (long long)gridDim.x * blockDim.y) {
+    const uint16_t* from = src + (per > 0 ? r / per * stride + r % per * ld : r * ld);
+    for (int k = threadIdx.x; k < units; k += blockDim.x) {
+      uint4 v;
+      uint16_t* e = reinterpret_cast<uint16_t*>(&v);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) e[i] = k * 8 + i < cols ? from[k * 8 + i] : (uint16_t)0;
+      dst[r * units + k] = v;
+    }
+  }
+}
+
 }  // namespace expk
 }  // namespace tc
 
@@ -683,17 +725,69 @@ static long long most_tiles(const ExpertDesc& g, int tiles_f, int tiles_c) {
   return tiles_f * std::min<long long>(g.rows, g.rows / tc::expk::tile_tokens(use_pairs(g)) + g.experts);
 }
 
+// Whether TMA can address an operand: 16-byte base and pitch, and an expert
+// stride that is a 16-byte multiple and not zero (shared weights).
+static bool tma_a(const ExpertDesc& g) { return tc::expk::on16(g.a, g.ld_a, 2); }
+static bool tma_b(const ExpertDesc& g) {
+  return tc::expk::on16(g.b, g.ld_b, 2) &&
+         (g.kind == kWeightGrad || g.experts == 1 || (g.stride_b * 2 % 16 == 0 && g.stride_b > 0));
+}
+
+// Packed copies: rows of a multiple of 8 elements.
+static long long packed_ld(int cols) { return (cols + 7) / 8 * 8; }
+static size_t packed_bytes(long long rows, int cols) { return (size_t)((rows * packed_ld(cols) * 2 + 255) / 256 * 256); }
+static int cols_a(const ExpertDesc& g) { return g.kind == kForward ? g.inner : g.outer; }
+static long long rows_b(const ExpertDesc& g) { return g.kind == kWeightGrad ? g.rows : (long long)g.experts * g.outer; }
+
+// Operands that TMA cannot address are copied into rows that it can, where the
+// product is large enough to pay for it.  Against the CUDA cores: 0.13 GFLOP (256
+// rows over 4 experts, 511 to 509 wide) 31 us against 40 (forward) and 21 (weight
+// gradient), 0.27 GFLOP 26 against 43 and 34, 137 GFLOP (32768 rows over 32
+// experts, 2047 to 1021) 219 against 9681.
+size_t expert_pack_bytes(const ExpertDesc& g) {
+  if ((g.dtype != kBF16 && g.dtype != kFP16) || (tma_a(g) && tma_b(g))) return 0;
+  if (2.0 * g.rows * g.inner * (double)g.outer < tc::expk::PACK_FLOPS) return 0;
+  size_t n = 0;
+  if (!tma_a(g)) n += packed_bytes(g.rows, cols_a(g));
+  if (!tma_b(g)) n += packed_bytes(rows_b(g), g.inner);
+  return n + 256;
+}
+
+static int pack_rows(const void* src, long long ld, long long stride, int per, long long rows, int cols, void* dst,
+                     cudaStream_t s) {
+  const int units = (int)(packed_ld(cols) / 8);
+  dim3 block(32, 8);
+  while ((int)block.x < units && block.x < 256) { block.x *= 2; block.y /= 2; }
+  const unsigned grid = (unsigned)std::min<long long>((rows + block.y - 1) / block.y, 148LL * 32);
+  tc::expk::expert_pack_kernel<<<grid, block, 0, s>>>(reinterpret_cast<const uint16_t*>(src), ld, stride, per, rows, cols,
+                                                      units, reinterpret_cast<uint4*>(dst));
+  return (int)cudaGetLastError();
+}
+
+int expert_tc_packed(const ExpertDesc& g, void* ws, cudaStream_t s) {
+  ExpertDesc d = g;
+  char* at = reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(ws) + 255) & ~uintptr_t(255));
+  int rc = 0;
+  if (!tma_a(g)) {
+    if ((rc = pack_rows(g.a, g.ld_a, 0, 0, g.rows, cols_a(g), at, s))) return rc;
+    d.a = at;
+    d.ld_a = packed_ld(cols_a(g));
+    at += packed_bytes(g.rows, cols_a(g));
+  }
+  if (!tma_b(g)) {
+    const bool weights = g.kind != kWeightGrad;
+    if ((rc = pack_rows(g.b, g.ld_b, weights ? g.stride_b : 0, weights ? g.outer : 0, rows_b(g), g.inner, at, s))) return rc;
+    d.b = at;
+    d.ld_b = packed_ld(g.inner);
+    d.stride_b = g.outer * d.ld_b;
+  }
+  return expert_tc(d, s);
+}
+
 bool expert_tc_ok(const ExpertDesc& g) {
   using namespace tc::expk;
   if (g.dtype != kBF16 && g.dtype != kFP16) return false;
-  const int des = dtype_size(g.d_dtype);
-  if (!on16(g.a, g.ld_a, 2) || !on16(g.b, g.ld_b, 2) || !on16(g.d, g.ld_d, des)) return false;
-  // expert strides: TMA wants 16-byte multiples, and no zero (shared weights)
-  if (g.kind == kWeightGrad) {
-    if (g.experts > 1 && (g.stride_d * des % 16 != 0 || g.stride_d == 0)) return false;
-  } else {
-    if (g.experts > 1 && (g.stride_b * 2 % 16 != 0 || g.stride_b == 0)) return false;
-  }
+  if (!tma_a(g) || !tma_b(g)) return false;
   const int F = g.kind == kInputGrad ? g.inner : g.outer;
   const int rows = tile_rows(use_pairs(g));
   return most_tiles(g, (F + rows - 1) / rows, (g.inner + 255) / 256) <= 0x7fffffffLL;
@@ -710,7 +804,9 @@ int expert_tc(const ExpertDesc& g, cudaStream_t s) {
   const bool pairs = use_pairs(g);
   p.tiles_f = (p.F + tile_rows(pairs) - 1) / tile_rows(pairs);
   p.tiles_c = (p.C + 255) / 256;
-  p.D = g.d; p.ldd = g.ld_d; p.d_dtype = g.d_dtype;
+  p.D = g.d; p.ldd = g.ld_d; p.stride_d = g.stride_d;
+  const int des = dtype_size(g.d_dtype);
+  p.d_vec = on16(g.d, g.ld_d, des) && (g.kind != kWeightGrad || g.experts == 1 || (g.stride_d * des % 16 == 0 && g.stride_d > 0));
   p.accumulate = g.accumulate;
   p.err = g.status;
   p.timeout_ns = wait_timeout_ns();
@@ -718,20 +814,21 @@ int expert_tc(const ExpertDesc& g, cudaStream_t s) {
   EMaps m;
   bool ok = true;
   if (g.kind == kWeightGrad) {
-    // both operands are read along their columns: 64-column boxes of 64 rows.
-    // Without rows nothing is loaded; the maps then cover the result
-    const bool none = g.rows == 0;
-    ok = ok && encode_map(&m.a, g.dtype, none ? g.d : g.a, none ? 8 : g.outer, none ? 1 : g.rows, 1, none ? 8 : g.ld_a, none ? 8 : g.ld_a, 64, BK);
-    ok = ok && encode_map(&m.b[0], g.dtype, none ? g.d : g.b, none ? 8 : g.inner, none ? 1 : g.rows, 1, none ? 8 : g.ld_b, none ? 8 : g.ld_b, 64, BK);
+    // both operands are read along their columns: 64-column boxes of 64 rows
+    ok = ok && encode_map(&m.a, g.dtype, g.a, g.outer, g.rows, 1, g.ld_a, g.ld_a, 64, BK);
+    ok = ok && encode_map(&m.b[0], g.dtype, g.b, g.inner, g.rows, 1, g.ld_b, g.ld_b, 64, BK);
     for (int i = 1; i < 4; ++i) m.b[i] = m.b[0];
-    ok = ok && encode_map(&m.d, g.d_dtype, g.d, g.inner, g.outer, g.experts, g.ld_d, g.experts > 1 ? g.stride_d : g.ld_d,
-                          g.d_dtype == kFP32 ? 16 : 32, 32, kTmaSw64);
+    if (p.d_vec)
+      ok = ok && encode_map(&m.d, g.d_dtype, g.d, g.inner, g.outer, g.experts, g.ld_d, g.experts > 1 ? g.stride_d : g.ld_d,
+                            g.d_dtype == kFP32 ? 16 : 32, 32, kTmaSw64);
+    else m.d = m.a;  // not used
   } else {
     const long long stride = g.experts > 1 ? g.stride_b : g.ld_b;
     ok = ok && (g.kind == kForward ? encode_map(&m.a, g.dtype, g.b, g.inner, g.outer, g.experts, g.ld_b, stride, BK, BM)
                                    : encode_map(&m.a, g.dtype, g.b, g.inner, g.outer, g.experts, g.ld_b, stride, 64, BK));
     for (int i = 0; i < 4; ++i) ok = ok && encode_map(&m.b[i], g.dtype, g.a, p.K, g.rows, 1, g.ld_a, g.ld_a, BK, 16 << i);
-    ok = ok && encode_map(&m.d, g.d_dtype, g.d, p.F, g.rows, 1, g.ld_d, g.ld_d, 32, 32, kTmaSw64);
+    if (p.d_vec) ok = ok && encode_map(&m.d, g.d_dtype, g.d, p.F, g.rows, 1, g.ld_d, g.ld_d, 32, 32, kTmaSw64);
+    else m.d = m.a;  // not used
   }
   if (!ok) return (int)cudaErrorInvalidValue;
   const bool bf = g.dtype == kBF16;

@@ -54,7 +54,7 @@ def test_route_refusals(lib):
 
 def test_product_refusals(lib):
     fwd = dict(xs=P, ld_xs=64, w=P, ld_w=64, stride_w=64 * 32, offsets=P, experts=4, rows=10, inner=64, outer=32, dtype=0,
-               y=P, ld_y=32, status=None)
+               y=P, ld_y=32, ws=None, ws_bytes=0, status=None)
     for change, rc in ((dict(xs=None), -1), (dict(ld_xs=63), -1), (dict(w=P + 1), -1), (dict(ld_w=1), -1),
                        (dict(stride_w=-1), -1), (dict(offsets=None), -1), (dict(offsets=P + 2), -1), (dict(experts=0), -1),
                        (dict(experts=1025), -1), (dict(rows=-1), -1), (dict(inner=0), -1), (dict(outer=0), -1),
@@ -65,11 +65,28 @@ def test_product_refusals(lib):
     for change, rc in ((dict(ld_xs=31), -1), (dict(ld_y=63), -1), (dict(dtype=9), -2), (dict(offsets=None), -1)):
         assert lib.muon_expert_input_grad(*dict(dgrad, **change).values(), None) == rc, change
     wgrad = dict(dys=P, ld_dys=32, xs=P, ld_xs=64, offsets=P, experts=4, rows=10, inner=64, outer=32, dtype=0, dw=P, ld_dw=64,
-                 stride_dw=64 * 32, dw_dtype=0, accumulate=0, status=None)
+                 stride_dw=64 * 32, dw_dtype=0, accumulate=0, ws=None, ws_bytes=0, status=None)
     for change, rc in ((dict(dys=None), -1), (dict(xs=P + 1), -1), (dict(ld_dw=63), -1), (dict(dw=None), -1),
                        (dict(dw_dtype=1), -2), (dict(accumulate=1), -2), (dict(dtype=1), -2), (dict(stride_dw=0), -1),
                        (dict(stride_dw=-8), -1), (dict(dw_dtype=2, dw=P + 2), -1)):
         assert lib.muon_expert_weight_grad(*dict(wgrad, **change).values(), None) == rc, change
+
+
+def test_workspaces_of_products(lib):
+    """Only large 16-bit products with an operand that TMA cannot address take one: its rows, padded to 8 elements."""
+    size = lib.muon_expert_workspace_size
+    ok = dict(kind=0, a=P, ld_a=1024, b=P, ld_b=1024, stride_b=1024 * 512, experts=4, rows=2048, inner=1024, outer=512, dtype=0)
+    assert size(*ok.values()) == 0
+    rows, weights = 2048 * 1024 * 2, 4 * 512 * 1024 * 2
+    for change, least in ((dict(a=P + 2), rows), (dict(ld_a=1025), rows), (dict(b=P + 8), weights), (dict(ld_b=1030), weights),
+                          (dict(stride_b=1024 * 512 + 4), weights), (dict(stride_b=0), weights),
+                          (dict(a=P + 2, ld_b=1028), rows + weights), (dict(kind=2, a=P + 2), 2048 * 512 * 2)):
+        assert least <= size(*dict(ok, **change).values()) <= least + 1024, change
+    odd = size(*dict(ok, inner=1021, ld_a=1021, ld_b=1021, stride_b=1021 * 512).values())
+    assert rows + weights <= odd <= rows + weights + 1024  # 1021 columns in rows of 1024
+    for change in (dict(a=P + 2, rows=4), dict(a=P + 2, dtype=2), dict(a=P + 2, kind=3), dict(a=P + 2, rows=-1),
+                   dict(a=P + 2, experts=0), dict(a=P + 2, dtype=7), dict(a=P + 2, inner=0)):
+        assert size(*dict(ok, **change).values()) == 0, change
 
 
 def _block_group(ptr=P, rows=64, cols=128, count=2, down=1, across=1, wdt=0, gdt=0, ld=(256, 256, 256)):

@@ -199,6 +199,44 @@ def test_products_of_odd_widths_and_pitches(inner, outer, pad, dtype):
                    U_NEAREST if dtype == SF else U_TRUNCATED)
 
 
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("counts,inner,outer,pad", [([300, 0, 511, 37], 1021, 515, 0), ([700, 130], 770, 1023, 1),
+                                                    ([90] * 12, 520, 1030, 4), ([40, 17, 2000], 336, 703, 0)])
+def test_large_products_of_odd_widths(counts, inner, outer, pad, dtype):
+    """Copied into aligned rows for the tensor cores; the results have rows of any alignment."""
+    case = product_case(22, counts, inner, outer, dtype, pad=pad)
+    nsm.muon_profile_begin()
+    check_products(*case, U_TRUNCATED, SF if pad else None)
+    prof = {r["kernel"]: r["launches"] for r in nsm.muon_profile_end()}
+    assert prof == {"expert_product": 3}
+    offsets, xs, dys, _ = case
+    base = randn(gen(23), len(counts), outer, inner + 1)[:, :, 1:]
+    out = base.clone()
+    store = torch.full((len(counts), outer, inner + 3), 7.0, device="cuda")
+    view = store[:, :, 1:inner + 1]
+    view.copy_(base)
+    nsm.muon_expert_weight_grad(dys, xs, offsets, out=view, accumulate=True)
+    one = nsm.muon_expert_weight_grad(dys, xs, offsets, out_dtype=SF)
+    for e, (lo, hi) in enumerate(segments(offsets, xs.shape[0])):
+        d, x = f64(dys[lo:hi]), f64(xs[lo:hi])
+        close(view[e], f64(out[e]) + d.T @ x, hi - lo + 1, f64(out[e]).abs() + d.abs().T @ x.abs(), U_TRUNCATED)
+        close(one[e], d.T @ x, hi - lo, d.abs().T @ x.abs(), U_TRUNCATED)
+    assert bool((store[:, :, 0] == 7).all()) and bool((store[:, :, inner + 1:] == 7).all())
+
+
+@pytest.mark.parametrize("dtype", [BF, HF, SF])
+def test_products_of_shared_weights(dtype):
+    """One matrix for all experts (a stride of zero), small and large."""
+    for counts, inner, outer in (([20, 0, 31], 64, 72), ([400, 0, 511], 768, 640)):
+        offsets, xs, _, w = product_case(24, counts, inner, outer, dtype)
+        shared = w[:1].expand(len(counts), outer, inner)
+        y, ref = (nsm.muon_expert_product(xs, v, offsets) for v in (shared, shared.contiguous()))
+        used = sum(counts)
+        x, m = f64(xs[:used]), f64(w[0])
+        close(y[:used], x @ m.T, inner, x.abs() @ m.abs().T, U_NEAREST if dtype == SF else U_TRUNCATED)
+        close(ref[:used], x @ m.T, inner, x.abs() @ m.abs().T, U_NEAREST if dtype == SF else U_TRUNCATED)
+
+
 @pytest.mark.parametrize("dtype", [BF, SF])
 def test_products_of_strided_weights(dtype):
     """Weights that are part of a fused stack: every second half of the rows, a slice of the columns; dW written into one."""
