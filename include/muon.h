@@ -152,7 +152,7 @@ MUON_API int muon_step(const muon_group* groups, int n_groups, const muon_hparam
  * (rows that all start on 16 bytes are moved by 16-byte accesses, others element
  * by element).  Nothing outside the blocks is read or written; blocks of one
  * call must not overlap.  Blocks count in the order of the groups, their
- * matrices, block rows and block columns. */
+ * matrices, block rows and block columns; a group has at most 2^20. */
 typedef struct {
   int rows, cols, count;
   int down, across;
@@ -165,7 +165,10 @@ typedef struct {
 
 /* muon_step with every block as a matrix of its own: its own norm, its own
  * orthogonalisation, and the update scale sqrt(max(rows, cols)) of the block.
- * A block that is a whole dense matrix gets muon_step's result, bit for bit. */
+ * The results are muon_step's on dense copies of the blocks, bit for bit, except
+ * for blocks with min(rows, cols) <= 128 and max <= 4096 in 16-bit standard chains
+ * of at most 64 iterations: they run in one launch, which adds up X X^T in another
+ * order, and differ by the chain's roundings. */
 MUON_API size_t muon_blocks_workspace_size(const muon_block_group* groups, int n_groups, const muon_hparams* hp);
 MUON_API size_t muon_blocks_workspace_min(const muon_block_group* groups, int n_groups, const muon_hparams* hp);
 MUON_API int muon_step_blocks(const muon_block_group* groups, int n_groups, const muon_hparams* hp, void* ws,
@@ -223,7 +226,7 @@ MUON_API int muon_ns_batched_noalloc(void* const* X, int count, int rows, int co
  * and the 16-bit products' operands need it for the tensor cores (see there).
  * Sorted rows that no expert owns are neither read into a result nor written.  All sums are held
  * in fp32 and rounded once, in an order that does not change from call to call.
- * Row counts and tokens * topk are at most 2^31 - 1, experts at most 1024.
+ * Rows, columns and tokens * topk are at most 2^30, experts at most 1024.
  *
  * muon_expert_sort: ids is tokens x topk of int32 or int64 (id_bytes 4 or 8),
  * row pitch ld_ids; an id outside [0, experts) goes to no expert.  The sort is
@@ -291,7 +294,8 @@ MUON_API int muon_expert_weight_grad(const void* dys, long long ld_dys, const vo
 MUON_API double muon_ns_flops(int rows, int cols, const muon_ns_params* ns);
 
 /* Opt-in launch profiler (tracing aid).  Between muon_profile_begin() and
- * muon_profile_end(), every kernel the library launches is bracketed by a pair
+ * muon_profile_end(), every kernel the library launches (the one to three of an
+ * expert-layer call together) is bracketed by a pair
  * of CUDA events recorded on the launch stream; this is the only state the
  * library keeps between calls, and only while profiling is on.
  * muon_profile_end synchronises on those events and fills up to max_entries

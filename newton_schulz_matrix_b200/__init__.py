@@ -540,6 +540,8 @@ class MuonStep:
         self.count = len(self.order)
 
     def __call__(self, stream=None) -> None:
+        if not _here(self.workspace.device, None):  # the tensors' device, not the current one
+            return _elsewhere(self.workspace.device, stream, self)
         rc = self._step(self._groups, self._ng, ctypes.byref(self._h), ctypes.c_void_p(self.workspace.data_ptr()),
                         ctypes.c_size_t(self.workspace.numel()), ctypes.c_void_p(self.status.data_ptr()),
                         ctypes.c_void_p(_stream_handle(stream)))
@@ -989,7 +991,8 @@ class ExpertMuonStep:
     workspace instead of a gradient per parameter.  The result is that of
     muon_expert_weight_grad followed by muon_step_blocks.  ``grad_dtype``: the
     buffer's type, the operands' (default: each stack's own) or float32.
-    ``blocks`` as for muon_step_blocks, one entry per stack.
+    ``blocks`` as for muon_step_blocks, one entry per stack.  Calls share the
+    buffer and the workspace and must not overlap on the GPU.
     """
 
     def __init__(self, params, moms, *, blocks: Sequence | None = None, slice_bytes: int = 512 << 20,
@@ -1004,7 +1007,7 @@ class ExpertMuonStep:
                 raise MuonError("params must be (experts, outer, inner) stacks on one device")
         self.device = params[0].device
         self.shapes = [tuple(w.shape) for w in params]
-        dtypes = [grad_dtype or w.dtype for w in params]
+        dtypes = self.dtypes = [grad_dtype or w.dtype for w in params]
         self.slices = []  # (stack, first expert, last expert)
         most = 0
         for i, w in enumerate(params):
@@ -1028,9 +1031,16 @@ class ExpertMuonStep:
     def __call__(self, factors, stream=None) -> None:
         if len(factors) != len(self.shapes):
             raise MuonError("factors must have one (dys, xs, offsets) per stack")
-        for (experts, outer, inner), (dys, xs, offsets) in zip(self.shapes, factors):
-            if offsets.numel() != experts + 1 or dys.shape[-1] != outer or xs.shape[-1] != inner:
-                raise MuonError("a stack's dys, xs and offsets do not fit its experts x outer x inner")
+        # everything is checked before the first slice steps
+        for i, ((experts, outer, inner), (dys, xs, offsets)) in enumerate(zip(self.shapes, factors)):
+            device, dtype, _, rows, cols, _ = _lead(dys, f"dys {i}")
+            if device != self.device or cols != outer:
+                raise MuonError(f"dys {i} must have {outer} columns on {self.device}")
+            _matrix(xs, f"xs {i}", device, dtype, rows, inner)
+            if _offsets_arg(offsets, device) != experts:
+                raise MuonError(f"offsets {i} must have {experts + 1} entries")
+            if self.dtypes[i] not in (dtype, torch.float32):
+                raise MuonError(f"gradients {i} are held in {self.dtypes[i]}, dys is {dtype}")
 
         if not _here(self.device, stream):
             return _elsewhere(self.device, stream, self, factors)

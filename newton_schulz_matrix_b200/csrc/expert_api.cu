@@ -25,12 +25,14 @@ bool matrix_ok(const void* p, long long ld, long long cols, int dtype) {
   return p != nullptr && element_aligned(p, dtype) && ld >= cols && ld <= (1LL << 40);
 }
 
-constexpr long long kMaxRows = 0x7fffffffLL;
+// Rows, columns and assignments of one call: kernels step through them with
+// 32-bit indices that must not wrap on the last step.
+constexpr long long kMaxRows = 1LL << 30;
 
 // Sizes shared by the gather, the combine and its gradients.
 int check_route(const int* slot, int tokens, int topk, int cols, long long rows, int dtype, const void* weights,
                 int w_dtype) {
-  if (tokens < 0 || topk <= 0 || cols <= 0 || rows < 0 || rows > kMaxRows) return MUON_ERR_INVALID;
+  if (tokens < 0 || topk <= 0 || cols <= 0 || cols > kMaxRows || rows < 0 || rows > kMaxRows) return MUON_ERR_INVALID;
   if ((long long)tokens * topk > kMaxRows) return MUON_ERR_INVALID;
   if (!dtype_ok(dtype) || (weights != nullptr && !dtype_ok(w_dtype))) return MUON_ERR_UNSUPPORTED;
   if (tokens == 0) return MUON_OK;
@@ -47,7 +49,8 @@ RouteArgs route(const int* slot, int tokens, int topk, int cols, long long rows,
 }
 
 int check_product(const int* offsets, int experts, long long rows, int inner, int outer, int dtype) {
-  if (experts <= 0 || experts > kMaxExperts || rows < 0 || rows > kMaxRows || inner <= 0 || outer <= 0)
+  if (experts <= 0 || experts > kMaxExperts || rows < 0 || rows > kMaxRows || inner <= 0 || outer <= 0 ||
+      inner > kMaxRows || outer > kMaxRows)
     return MUON_ERR_INVALID;
   if (!dtype_ok(dtype)) return MUON_ERR_UNSUPPORTED;
   if (offsets == nullptr || !element_aligned(offsets, MUON_FP32)) return MUON_ERR_INVALID;
@@ -155,7 +158,7 @@ int muon_expert_combine_backward(const void* dy, long long ld_dy, const void* ys
 size_t muon_expert_workspace_size(int kind, const void* a, long long ld_a, const void* b, long long ld_b,
                                   long long stride_b, int experts, long long rows, int inner, int outer, int dtype) {
   if (kind < MUON_EXPERT_PRODUCT || kind > MUON_EXPERT_WEIGHT_GRAD || experts <= 0 || experts > kMaxExperts || rows <= 0 ||
-      rows > kMaxRows || inner <= 0 || outer <= 0 || !dtype_ok(dtype))
+      rows > kMaxRows || inner <= 0 || outer <= 0 || inner > kMaxRows || outer > kMaxRows || !dtype_ok(dtype))
     return 0;
   const ExpertDesc g{kind, nullptr, experts, rows, inner, outer, dtype, a, ld_a, b, ld_b, stride_b, nullptr, 0, 0, dtype, 0,
                      nullptr};

@@ -204,7 +204,7 @@ expert_rank_kernel(const SortArgs a, int n, int run, int warps, const int* __res
       at += __popc(same & ((1u << lane) - 1u));
       if (i < p1) {
         a.slot[i] = key[q] < E ? at : -1;
-        a.source[at] = i;
+        if (at < n) a.source[at] = i;  // ids that change under the sort write nothing out of range
       }
       __syncwarp();
     }

@@ -790,7 +790,7 @@ bool expert_tc_ok(const ExpertDesc& g) {
   if (!tma_a(g) || !tma_b(g)) return false;
   const int F = g.kind == kInputGrad ? g.inner : g.outer;
   const int rows = tile_rows(use_pairs(g));
-  return most_tiles(g, (F + rows - 1) / rows, (g.inner + 255) / 256) <= 0x7fffffffLL;
+  return most_tiles(g, (F + rows - 1) / rows, (g.inner + 255) / 256) <= (1LL << 30);
 }
 
 int expert_tc(const ExpertDesc& g, cudaStream_t s) {

@@ -21,7 +21,7 @@ def test_sort_refusals(lib):
     size = lib.muon_expert_sort_workspace_size
     assert size(32, 8, 216) > 0 and size(0, 1, 1) > 0
     assert size(1 << 20, 8, 64) > 256  # several runs count apart
-    for bad in ((-1, 8, 64), (32, 0, 64), (32, 8, 0), (32, 8, nsm.EXPERT_MAX + 1), (1 << 30, 8, 64)):
+    for bad in ((-1, 8, 64), (32, 0, 64), (32, 8, 0), (32, 8, nsm.EXPERT_MAX + 1), (1 << 30, 8, 64), (1 << 27, 9, 64)):
         assert size(*bad) == 0
     ok = dict(ids=P, es=8, ld=8, tokens=1 << 17, topk=8, experts=64, offsets=P, slot=P, source=P, ws=P, bytes=0)
     # the workspace is too small: every other argument is right
@@ -38,7 +38,7 @@ def test_route_refusals(lib):
     for change, rc in ((dict(ld_x=63), -1), (dict(x=None), -1), (dict(x=P + 1), -1), (dict(slot=None), -1),
                        (dict(slot=P + 2), -1), (dict(topk=0), -1), (dict(cols=0), -1), (dict(tokens=-1), -1),
                        (dict(dtype=3), -2), (dict(xs=P + 1), -1), (dict(ld_xs=10), -1), (dict(rows=-1), -1),
-                       (dict(rows=1 << 31), -1), (dict(dtype=2, x=P + 2), -1), (dict(tokens=1 << 30, topk=4), -1)):
+                       (dict(rows=(1 << 30) + 1), -1), (dict(cols=(1 << 30) + 1, ld_x=1 << 31, ld_xs=1 << 31), -1), (dict(dtype=2, x=P + 2), -1), (dict(tokens=1 << 30, topk=4), -1)):
         assert lib.muon_expert_gather(*dict(gather, **change).values(), None) == rc, change
     assert lib.muon_expert_gather(*dict(gather, tokens=0, slot=None, x=None).values(), None) == 0
     combine = dict(ys=P, ld_ys=64, rows=8, slot=P, w=P, wdt=2, tokens=4, topk=2, cols=64, dtype=0, y=P, ld_y=64)

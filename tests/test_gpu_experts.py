@@ -1,6 +1,10 @@
 """The expert-layer operators against plain 64-bit versions: routing (sort,
 gather, combine and gradients), the experts' products and their gradients, and
 a whole layer's training step into the Muon step."""
+import os
+import subprocess
+import sys
+
 import pytest
 import torch
 
@@ -9,6 +13,7 @@ import oracle
 from expert_util import U_NEAREST, U_TRUNCATED, close, f64, rows_ref, segments, sort_ref
 
 pytestmark = pytest.mark.gpu
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 BF, HF, SF = torch.bfloat16, torch.float16, torch.float32
 
 
@@ -333,6 +338,79 @@ def test_products_repeat_bit_for_bit_and_on_another_stream():
         assert torch.equal(first, other)
 
 
+def test_products_of_no_row():
+    offsets = torch.zeros(4, dtype=torch.int32, device="cuda")
+    for dtype in (BF, SF):
+        xs, dys, w = (torch.empty(s, dtype=dtype, device="cuda") for s in ((0, 64), (0, 72), (3, 72, 64)))
+        assert nsm.muon_expert_product(xs, w, offsets).shape == (0, 72)
+        assert nsm.muon_expert_input_grad(dys, w, offsets).shape == (0, 64)
+        assert not nsm.muon_expert_weight_grad(dys, xs, offsets).any()
+        out = torch.full((3, 72, 64), 7.0, device="cuda")
+        assert bool((nsm.muon_expert_weight_grad(dys, xs, offsets, out=out, accumulate=True) == 7).all())
+        y = nsm.muon_expert_combine(xs, torch.zeros(5, 2, dtype=torch.int32, device="cuda"))
+        assert y.shape == (5, 64) and not y.any()
+
+
+def test_rows_past_two_to_the_32_bytes_and_elements():
+    """The last rows of a matrix of more than 2^32 elements, in every operator."""
+    cols, rows = 4096, (1 << 20) + 4099
+    big = torch.empty(rows, cols, dtype=BF, device="cuda")
+    g = gen(41)
+    counts = [70, 0, 131, 3]
+    first = rows - sum(counts)
+    offsets = offsets_of(counts, first)
+    last = randn(g, sum(counts), cols, dtype=BF)
+    big[first:] = last
+    w = (randn(g, 4, 40, cols) / 64).to(BF)
+    near = offsets_of(counts)
+    y = nsm.muon_expert_product(big, w, offsets)
+    assert torch.equal(y[first:], nsm.muon_expert_product(last, w, near))
+    dys = torch.empty(rows, 40, dtype=BF, device="cuda")
+    dys[first:] = randn(g, sum(counts), 40, dtype=BF)
+    assert torch.equal(nsm.muon_expert_weight_grad(dys, big, offsets), nsm.muon_expert_weight_grad(dys[first:], last, near))
+    slot = (first + torch.randperm(sum(counts), generator=g, device="cuda")).to(torch.int32).view(-1, 2)
+    back = nsm.muon_expert_combine(big, slot)
+    assert torch.equal(back, nsm.muon_expert_combine(last, slot - first))
+    wts = torch.rand(*slot.shape, generator=g, device="cuda")
+    ref_dys, ref_dw = nsm.muon_expert_combine_backward(back, last, slot - first, wts)
+    got_dys, got_dw = nsm.muon_expert_combine_backward(back, big, slot, wts, out=big)
+    assert torch.equal(got_dw, ref_dw) and torch.equal(got_dys[first:], ref_dys)
+    nsm.muon_expert_gather(back, slot, out=big)
+    assert torch.equal(big[slot.long()], back[:, None].expand(-1, 2, -1))
+    wide = torch.empty(rows, cols, dtype=BF, device="cuda")
+    nsm.muon_expert_input_grad(dys, w, offsets, out=wide)
+    assert torch.equal(wide[first:], nsm.muon_expert_input_grad(dys[first:], w, near))
+
+
+def test_the_first_calls_of_a_process_can_be_captured():
+    """One-time set-up (shared-memory opt-ins, tensor maps) happens under a capture too."""
+    code = """
+import torch, sys
+sys.path.insert(0, {root!r})
+import newton_schulz_matrix_b200 as nsm
+x, w = torch.randn(64, 64, device="cuda").bfloat16(), torch.randn(4, 64, 64, device="cuda").bfloat16()
+ids, m = torch.randint(0, 4, (64, 2), device="cuda"), torch.zeros(4, 64, 64, device="cuda")
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    offsets, slot, _ = nsm.muon_expert_sort(ids, 4)
+    xs = nsm.muon_expert_gather(x, slot)
+    h = nsm.muon_expert_product(xs, w, offsets)
+    y = nsm.muon_expert_combine(h, slot)
+    dw = nsm.muon_expert_weight_grad(h, xs, offsets)
+    nsm.muon_step_blocks([w], [dw], [m], [(32, 64)])
+w0 = w.clone()
+g.replay()
+torch.cuda.synchronize()
+got = y.clone()
+w.copy_(w0)
+offsets, slot, _ = nsm.muon_expert_sort(ids, 4)
+h = nsm.muon_expert_product(nsm.muon_expert_gather(x, slot), w, offsets)
+assert torch.equal(got, nsm.muon_expert_combine(h, slot)) and got.any()
+""".format(root=ROOT)
+    subprocess.run([sys.executable, "-c", code], check=True, timeout=300, cwd=ROOT)
+
+
 # ---------------------------------------------------------------- together
 def layer(x, ids, probs, w1, w2, blocks_dtype=BF):
     """Forward and backward of a two-product expert layer with relu-squared between, and all that it leaves."""
@@ -441,6 +519,23 @@ def test_a_training_step_of_a_layer():
                 # 2e-2 of the step (the 16-bit chain's bar) and half a bf16 step of the weights
                 step_norm = 0.02 * 0.2 * max(r, c) ** 0.5 * torch.from_numpy(o).norm()
                 assert err <= 2e-2 * step_norm + 2.0 ** -8 * torch.from_numpy(ref).norm()
+
+
+def test_expert_step_refuses_before_it_steps():
+    g = gen(42)
+    w, m = randn(g, 2, 64, 32, dtype=BF), torch.zeros(2, 64, 32, device="cuda")
+    step = nsm.ExpertMuonStep([w, w.clone()], [m, m.clone()])
+    good = (randn(g, 8, 64, dtype=BF), randn(g, 8, 32, dtype=BF), offsets_of([3, 5]))
+    before = w.clone()
+    for bad in ((good[0][:7], good[1], good[2]), (good[0].half(), good[1].half(), good[2]), (good[0], good[1], good[2].long()),
+                (good[0], good[1], offsets_of([1, 2, 3])), (good[1], good[0], good[2]), (good[0].cpu(), good[1], good[2])):
+        with pytest.raises(nsm.MuonError):
+            step([good, bad])
+    with pytest.raises(nsm.MuonError):
+        step([good])
+    assert torch.equal(w, before) and not m.any()
+    step([good, good])
+    assert not torch.equal(w, before)
 
 
 def test_a_captured_layer_replays():
