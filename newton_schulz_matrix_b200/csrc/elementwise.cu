@@ -16,6 +16,7 @@
 // stay row-contiguous.
 #include "common.cuh"
 #include "internal.h"
+#include "tc_common.cuh"
 
 namespace muon {
 
@@ -24,6 +25,27 @@ constexpr int kPackThreads = 256;
 
 int pack_tiles(int rows, int cols) {
   return ((rows + kTile - 1) / kTile) * ((cols + kTile - 1) / kTile);
+}
+
+// The kernels around a chain follow each other directly on the stream: each may
+// be set up while the one before it drains (programmatic dependent launch) and
+// touches no memory before that one has finished.
+__device__ __forceinline__ void chain_step() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+template <typename Kernel, typename... Args>
+static void launch_step(Kernel kern, dim3 grid, int threads, cudaStream_t s, const Args&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = tc::programmatic_launch() ? 1 : 0;
+  cudaLaunchKernelEx(&cfg, kern, args...);  // the callers read the sticky error
 }
 
 template <typename T>
@@ -115,6 +137,7 @@ __device__ __forceinline__ float block_sum_fixed(float v, float* red) {
 template <typename TS, typename TX, bool MOMENTUM, bool TRANS>
 __global__ void __launch_bounds__(kPackThreads)
 pack_kernel(const PackArgs a, const __grid_constant__ SegmentPtrs p) {
+  chain_step();
   __shared__ float tile[TRANS ? kTile : 1][kTile + 1];
   __shared__ float red[kPackThreads / 32];
   const int b = blockIdx.y;
@@ -240,6 +263,7 @@ pack_kernel(const PackArgs a, const __grid_constant__ SegmentPtrs p) {
 // ----------------------------------------------------------------------------
 __global__ void __launch_bounds__(256)
 norm_kernel(const float* __restrict__ partials, int stride, int n, float eps, float* __restrict__ inv) {
+  chain_step();
   __shared__ double red[256];
   const int b = blockIdx.x;
   double s = 0.0;
@@ -259,6 +283,7 @@ norm_kernel(const float* __restrict__ partials, int stride, int n, float eps, fl
 template <typename TD, typename TX, bool UPDATE, bool TRANS>
 __global__ void __launch_bounds__(kPackThreads)
 unpack_kernel(const UnpackArgs a, const __grid_constant__ SegmentPtrs p) {
+  chain_step();
   __shared__ float tile[TRANS ? kTile : 1][kTile + 1];
   const int b = blockIdx.y;
   const int tcols = (a.cols + kTile - 1) / kTile;
@@ -351,11 +376,11 @@ static void pack_dispatch2(const PackArgs& a, const SegmentPtrs& p, cudaStream_t
   const bool trans = a.rows > a.cols;
   dim3 grid(pack_tiles(a.rows, a.cols), a.count);
   if (a.momentum_mode) {
-    if (trans) pack_kernel<TS, TX, true, true><<<grid, kPackThreads, 0, s>>>(a, p);
-    else pack_kernel<TS, TX, true, false><<<grid, kPackThreads, 0, s>>>(a, p);
+    if (trans) launch_step(pack_kernel<TS, TX, true, true>, grid, kPackThreads, s, a, p);
+    else launch_step(pack_kernel<TS, TX, true, false>, grid, kPackThreads, s, a, p);
   } else {
-    if (trans) pack_kernel<TS, TX, false, true><<<grid, kPackThreads, 0, s>>>(a, p);
-    else pack_kernel<TS, TX, false, false><<<grid, kPackThreads, 0, s>>>(a, p);
+    if (trans) launch_step(pack_kernel<TS, TX, false, true>, grid, kPackThreads, s, a, p);
+    else launch_step(pack_kernel<TS, TX, false, false>, grid, kPackThreads, s, a, p);
   }
 }
 
@@ -379,7 +404,7 @@ void launch_pack(const PackArgs& a, const SegmentPtrs& p, cudaStream_t s) {
 
 void launch_norm(const float* partials, int stride, int n, int count, float eps, float* inv, cudaStream_t s) {
   if (count <= 0) return;
-  norm_kernel<<<count, 256, 0, s>>>(partials, stride, n, eps, inv);
+  launch_step(norm_kernel, dim3(count), 256, s, partials, stride, n, eps, inv);
 }
 
 template <typename TD, typename TX>
@@ -387,11 +412,11 @@ static void unpack_dispatch2(const UnpackArgs& a, const SegmentPtrs& p, cudaStre
   dim3 grid(pack_tiles(a.rows, a.cols), a.count);
   const bool trans = a.rows > a.cols;
   if (a.update_mode) {
-    if (trans) unpack_kernel<TD, TX, true, true><<<grid, kPackThreads, 0, s>>>(a, p);
-    else unpack_kernel<TD, TX, true, false><<<grid, kPackThreads, 0, s>>>(a, p);
+    if (trans) launch_step(unpack_kernel<TD, TX, true, true>, grid, kPackThreads, s, a, p);
+    else launch_step(unpack_kernel<TD, TX, true, false>, grid, kPackThreads, s, a, p);
   } else {
-    if (trans) unpack_kernel<TD, TX, false, true><<<grid, kPackThreads, 0, s>>>(a, p);
-    else unpack_kernel<TD, TX, false, false><<<grid, kPackThreads, 0, s>>>(a, p);
+    if (trans) launch_step(unpack_kernel<TD, TX, false, true>, grid, kPackThreads, s, a, p);
+    else launch_step(unpack_kernel<TD, TX, false, false>, grid, kPackThreads, s, a, p);
   }
 }
 
@@ -414,6 +439,7 @@ void launch_unpack(const UnpackArgs& a, const SegmentPtrs& p, cudaStream_t s) {
 }
 
 __global__ void status_or_kernel(int* status, int count, const int* chunk_err) {
+  chain_step();
   const int i = blockIdx.x * blockDim.x + threadIdx.x;
   const int e = *chunk_err;
   if (i < count && e != 0) status[i] |= e;
@@ -421,7 +447,7 @@ __global__ void status_or_kernel(int* status, int count, const int* chunk_err) {
 
 void launch_status_or(int* status, int count, const int* chunk_err, cudaStream_t s) {
   if (count <= 0 || status == nullptr) return;
-  status_or_kernel<<<(count + 255) / 256, 256, 0, s>>>(status, count, chunk_err);
+  launch_step(status_or_kernel, dim3((count + 255) / 256), 256, s, status, count, chunk_err);
 }
 
 void launch_convert(const void* src, int sdt, void* dst, int ddt, long long n, cudaStream_t s) {
