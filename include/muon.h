@@ -226,7 +226,8 @@ MUON_API int muon_ns_batched_noalloc(void* const* X, int count, int rows, int co
  * and the 16-bit products' operands need it for the tensor cores (see there).
  * Sorted rows that no expert owns are neither read into a result nor written.  All sums are held
  * in fp32 and rounded once, in an order that does not change from call to call.
- * Rows, columns and tokens * topk are at most 2^30, experts at most 1024.
+ * Rows, columns and tokens * topk are at most 2^30, experts at most 1024 and
+ * experts * outer (all weights' rows) at most 2^34.
  *
  * muon_expert_sort: ids is tokens x topk of int32 or int64 (id_bytes 4 or 8),
  * row pitch ld_ids; an id outside [0, experts) goes to no expert.  The sort is

@@ -50,7 +50,7 @@ RouteArgs route(const int* slot, int tokens, int topk, int cols, long long rows,
 
 int check_product(const int* offsets, int experts, long long rows, int inner, int outer, int dtype) {
   if (experts <= 0 || experts > kMaxExperts || rows < 0 || rows > kMaxRows || inner <= 0 || outer <= 0 ||
-      inner > kMaxRows || outer > kMaxRows)
+      inner > kMaxRows || outer > kMaxRows || (long long)experts * outer > (1LL << 34))
     return MUON_ERR_INVALID;
   if (!dtype_ok(dtype)) return MUON_ERR_UNSUPPORTED;
   if (offsets == nullptr || !element_aligned(offsets, MUON_FP32)) return MUON_ERR_INVALID;

@@ -6,12 +6,17 @@
 // 128 x 128 output tiles with an 8 x 8 block of sums per thread (16384 fp32 rows
 // over 16 experts of 1408 x 2048: 35 TFLOP/s, bound by the FMA pipe and the
 // shared-memory reads beside it; 64 x 64 tiles 23), 64 x 64 with 4 x 4 or 32 x 32
-// with 2 x 2 where larger ones cannot occupy the SMs: the three products of 301
-// rows over 7 experts, 333 to 130 wide, take 39 us with 32 x 32 tiles and 73 with
-// 64 x 64.  The k steps go through shared memory, the next step's elements being
-// loaded into registers while this one is multiplied.  The tile list is read
-// from the offsets on the device: a block walks the experts' tiles of its own
-// index and stride, so nothing waits for the counts on the host.
+// with 2 x 2 where larger ones cannot occupy the SMs (15 rows over 2 experts, 1946
+// to 848 wide, forward: 62 us with 32 x 32 tiles, 140 with 64 x 64; 1610 rows over
+// 25 experts, 144 to 304 wide: 31 and 22) or the segments cannot fill them (2000
+// rows over 1024 experts, 64 to 64 wide: 56 us with 32 x 32, 78 with 128 x 128).
+// The k steps go through shared memory, the next step's elements being
+// loaded into registers while this one is multiplied.  The tile list comes from
+// the offsets on the device: every block keeps the segments and a running count
+// of tiles in shared memory, takes the tiles of its own index and stride and
+// finds their experts by bisection, so nothing waits for the counts on the host.
+// (Walking the offsets in memory instead cost each block a fifth of a microsecond
+// per expert: those 2000 rows 245 us, 203 rows over 64 experts 49 us for 19 now.)
 #include <algorithm>
 
 #include "common.cuh"
@@ -68,66 +73,93 @@ __device__ __forceinline__ void take(const float* s, float (&v)[S]) {
 }
 
 template <typename T, int TB, int TK>
-__global__ void __launch_bounds__(256, TB > 64 ? 2 : 1)
+__global__ void __launch_bounds__(256, 1)
 expert_simt_kernel(const ExpertDesc g) {
   __shared__ __align__(16) float As[TK][TB + 4];
   __shared__ __align__(16) float Bs[TK][TB + 4];
+  __shared__ int seg_lo[kMaxExperts], seg_len[kMaxExperts], rows_before[kMaxExperts + 1];
   constexpr int S = TB / 16;  // sums per thread and direction
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   const T* ga = reinterpret_cast<const T*>(g.a);
   const T* gb = reinterpret_cast<const T*>(g.b);
-  long long next = blockIdx.x;  // this block's next tile, counted over all experts
-  long long first = 0;          // tiles of the experts before e
-  for (int e = 0; e < g.experts; ++e) {
-    const long long lo = min(max((long long)g.offsets[e], 0LL), g.rows);
-    const long long hi = min(max((long long)g.offsets[e + 1], lo), g.rows);
-    const int count = (int)(hi - lo);
-    const int M = g.kind == kWeightGrad ? g.outer : count;
-    const int N = g.kind == kInputGrad || g.kind == kWeightGrad ? g.inner : g.outer;
-    const int K = g.kind == kForward ? g.inner : g.kind == kInputGrad ? g.outer : count;
-    const long long tn = (N + TB - 1) / TB, tiles = ((M + TB - 1) / TB) * tn;
-    for (; next < first + tiles; next += gridDim.x) {
-      const int i0 = (int)((next - first) / tn) * TB, j0 = (int)((next - first) % tn) * TB;
-      const T* a = ga + lo * g.ld_a;
-      const T* b = gb + (g.kind == kWeightGrad ? lo * g.ld_b : e * g.stride_b);
-      const Operand A = g.kind == kWeightGrad ? Operand{a, 1, g.ld_a, M, K} : Operand{a, g.ld_a, 1, M, K};
-      const Operand B = g.kind == kForward ? Operand{b, g.ld_b, 1, N, K} : Operand{b, 1, g.ld_b, N, K};
-      float acc[S][S] = {};
-      float ra[TB * TK / 256], rb[TB * TK / 256];
-      fetch<T, TB, TK>(A, i0, 0, ra);
-      fetch<T, TB, TK>(B, j0, 0, rb);
-      for (int k0 = 0; k0 < K; k0 += TK) {
-        put<TB, TK>(A, ra, As);
-        put<TB, TK>(B, rb, Bs);
-        __syncthreads();
-        if (k0 + TK < K) {
-          fetch<T, TB, TK>(A, i0, k0 + TK, ra);
-          fetch<T, TB, TK>(B, j0, k0 + TK, rb);
-        }
-#pragma unroll (TB > 64 ? 8 : TK)
-        for (int kk = 0; kk < TK; ++kk) {
-          float av[S], bv[S];
-          take<S>(&As[kk][ty * S], av);
-          take<S>(&Bs[kk][tx * S], bv);
+  const bool wg = g.kind == kWeightGrad;
+  const int N = g.kind == kForward ? g.outer : g.inner;
+  const long long tn = (N + TB - 1) / TB;
+  for (int e = threadIdx.x; e < g.experts; e += blockDim.x) {
+    const int lo = (int)min(max((long long)g.offsets[e], 0LL), g.rows);
+    seg_lo[e] = lo;
+    seg_len[e] = (int)min(max((long long)g.offsets[e + 1], (long long)lo), g.rows) - lo;
+  }
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    // running counts of tile rows, 32 experts at a time
+    const int lane = threadIdx.x;
+    int sum = 0;
+    for (int e0 = 0; e0 < g.experts; e0 += 32) {
+      const int e = e0 + lane;
+      int incl = e < g.experts ? ((wg ? g.outer : seg_len[e]) + TB - 1) / TB : 0;
 #pragma unroll
-          for (int i = 0; i < S; ++i)
-#pragma unroll
-            for (int j = 0; j < S; ++j) acc[i][j] = fmaf(av[i], bv[j], acc[i][j]);
-        }
-        __syncthreads();
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
       }
-      const long long base = g.kind == kWeightGrad ? e * g.stride_d : lo * g.ld_d;
-#pragma unroll
-      for (int i = 0; i < S; ++i)
-#pragma unroll
-        for (int j = 0; j < S; ++j) {
-          const int r = i0 + ty * S + i, c = j0 + tx * S + j;
-          if (r >= M || c >= N) continue;
-          const long long at = base + r * g.ld_d + c;
-          store_any(g.d, at, g.d_dtype, g.accumulate ? load_any(g.d, at, g.d_dtype) + acc[i][j] : acc[i][j]);
-        }
+      if (e < g.experts) rows_before[e + 1] = sum + incl;
+      sum += __shfl_sync(0xffffffffu, incl, 31);
     }
-    first += tiles;
+    if (lane == 0) rows_before[0] = 0;
+  }
+  __syncthreads();
+  const long long total = rows_before[g.experts] * tn;
+#pragma unroll 1
+  for (long long next = blockIdx.x; next < total; next += gridDim.x) {
+    const int tile_row = (int)(next / tn);
+    // its expert: the last one with rows_before[e] <= tile_row (empty ones repeat a count)
+    int e = 0;
+    for (int past = g.experts; past - e > 1;) {
+      const int mid = (e + past) >> 1;
+      if (rows_before[mid] <= tile_row) e = mid; else past = mid;
+    }
+    const int M = wg ? g.outer : seg_len[e];
+    const int K = g.kind == kForward ? g.inner : g.kind == kInputGrad ? g.outer : seg_len[e];
+    const int i0 = (tile_row - rows_before[e]) * TB, j0 = (int)(next % tn) * TB;
+    const T* a = ga + seg_lo[e] * g.ld_a;
+    const T* b = gb + (wg ? seg_lo[e] * g.ld_b : e * g.stride_b);
+    const Operand A = wg ? Operand{a, 1, g.ld_a, M, K} : Operand{a, g.ld_a, 1, M, K};
+    const Operand B = g.kind == kForward ? Operand{b, g.ld_b, 1, N, K} : Operand{b, 1, g.ld_b, N, K};
+    float acc[S][S] = {};
+    float ra[TB * TK / 256], rb[TB * TK / 256];
+    fetch<T, TB, TK>(A, i0, 0, ra);
+    fetch<T, TB, TK>(B, j0, 0, rb);
+    for (int k0 = 0; k0 < K; k0 += TK) {
+      put<TB, TK>(A, ra, As);
+      put<TB, TK>(B, rb, Bs);
+      __syncthreads();
+      if (k0 + TK < K) {
+        fetch<T, TB, TK>(A, i0, k0 + TK, ra);
+        fetch<T, TB, TK>(B, j0, k0 + TK, rb);
+      }
+#pragma unroll (TB > 64 ? 4 : TK)
+      for (int kk = 0; kk < TK; ++kk) {
+        float av[S], bv[S];
+        take<S>(&As[kk][ty * S], av);
+        take<S>(&Bs[kk][tx * S], bv);
+#pragma unroll
+        for (int i = 0; i < S; ++i)
+#pragma unroll
+          for (int j = 0; j < S; ++j) acc[i][j] = fmaf(av[i], bv[j], acc[i][j]);
+      }
+      __syncthreads();
+    }
+    const long long base = wg ? e * g.stride_d : seg_lo[e] * g.ld_d;
+#pragma unroll
+    for (int i = 0; i < S; ++i)
+#pragma unroll
+      for (int j = 0; j < S; ++j) {
+        const int r = i0 + ty * S + i, c = j0 + tx * S + j;
+        if (r >= M || c >= N) continue;
+        const long long at = base + r * g.ld_d + c;
+        store_any(g.d, at, g.d_dtype, g.accumulate ? load_any(g.d, at, g.d_dtype) + acc[i][j] : acc[i][j]);
+      }
   }
 }
 
@@ -139,9 +171,11 @@ int launch(const ExpertDesc& g, cudaStream_t s) {
     return tn * (g.kind == kWeightGrad ? (long long)g.experts * ((g.outer + t - 1) / t)
                                        : std::min<long long>(g.rows, g.rows / t + g.experts));
   };
+  // and the average length of a segment in the direction that the tiles cut
+  const long long fill = g.kind == kWeightGrad ? g.outer : g.rows / g.experts;
   const int sms = num_sms();
-  if (tiles(64) < 2 * sms) expert_simt_kernel<T, 32, 32><<<4 * sms, 256, 0, s>>>(g);
-  else if (tiles(128) < 2 * sms) expert_simt_kernel<T, 64, 32><<<4 * sms, 256, 0, s>>>(g);
+  if (tiles(64) < sms || fill <= 32) expert_simt_kernel<T, 32, 32><<<4 * sms, 256, 0, s>>>(g);
+  else if (tiles(128) < 2 * sms || fill <= 64) expert_simt_kernel<T, 64, 32><<<4 * sms, 256, 0, s>>>(g);
   else expert_simt_kernel<T, 128, 16><<<2 * sms, 256, 0, s>>>(g);
   return (int)cudaGetLastError();
 }

@@ -228,3 +228,11 @@ def test_block_groups_name_every_block_once():
     assert [g.W[i] - P for i in range(2)] == [0, 200] and [g.M[i] - P for i in range(2)] == [0, 96]
     g = groups[1]
     assert (g.rows, g.cols, g.count, g.down, g.across) == (4, 6, 2, 1, 1) and [g.W[i] - P for i in range(2)] == [0, 200]
+
+
+def test_products_of_too_many_weight_rows(lib):
+    """experts * outer is at most 2^34: above it tile counts would pass 32 bits."""
+    outer = (1 << 25) + 1
+    assert lib.muon_expert_product(P, 8, P, 8, 8 * outer, P, 512, 10, 8, outer, 0, P, outer, None, 0, None, None) == -1
+    assert lib.muon_expert_input_grad(P, outer, P, 8, 8 * outer, P, 512, 10, 8, outer, 0, P, 8, None, 0, None, None) == -1
+    assert lib.muon_expert_weight_grad(P, outer, P, 8, P, 512, 10, 8, outer, 0, P, 8, 8 * outer, 0, 0, None, 0, None, None) == -1
