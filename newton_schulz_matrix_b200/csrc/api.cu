@@ -557,6 +557,10 @@ UpdateSlots& slots_storage() {
   thread_local UpdateSlots slots;
   return slots;
 }
+PackSlots& pack_slots_storage() {
+  thread_local PackSlots slots;
+  return slots;
+}
 
 // MUON_CHAIN=1: 16-bit chains whose products all run on the paired-CTA kernel
 // go out as one persistent launch per (up to 24) products, with per-matrix
@@ -692,12 +696,14 @@ int run_batches(const std::vector<Batch>& batches, const std::vector<GroupView>&
           launch_pack(a, ptrs, s);
         }
       };
-      launch_pieces(prescale ? 1 : 0);
-      {
-        ProfScope ps(kProfNorm, 0.0, (double)chunk * L.tiles * 4 + chunk * 4.0, s);
-        launch_norm(B.partials, L.tiles, L.tiles, chunk, ns->eps, B.inv, s);
+      if (!one_launch) {
+        launch_pieces(prescale ? 1 : 0);
+        {
+          ProfScope ps(kProfNorm, 0.0, (double)chunk * L.tiles * 4 + chunk * 4.0, s);
+          launch_norm(B.partials, L.tiles, L.tiles, chunk, ns->eps, B.inv, s);
+        }
+        if (prescale) launch_pieces(2);
       }
-      if (prescale) launch_pieces(2);
       if (cudaGetLastError() != cudaSuccess) return MUON_ERR_CUDA;
       int used = 0;
       PlaneCache planes;
@@ -729,10 +735,26 @@ int run_batches(const std::vector<Batch>& batches, const std::vector<GroupView>&
           }
         }
         if (one_launch) {
-          const BlockChainArgs ba{L.n, L.m, chunk, ns->iters, prescale ? 0 : 1, cdt, B.X[0], L.ld_m, B.x_bs, B.inv,
-                                  ns->coeffs, B.err};
-          ProfScope ps(kProfBlockChain, flops_of(L.n, L.m, ns) * chunk, 2.0 * chunk * L.n * L.m * 3, s);
-          if (launch_ns_block(ba, us, s) != 0) return MUON_ERR_CUDA;
+          PackSlots& gs = pack_slots_storage();
+          double bytes = 0.0;
+          for (const Piece& pc : pieces) {
+            const GroupView& v = views[pc.group];
+            const void* const* src = v.src + pc.first;
+            float* const* mom = v.mom + pc.first;
+            const bool vec = rows16(src, pc.count, v.ld_src, v.src_dtype) &&
+                             rows16(reinterpret_cast<const void* const*>(mom), pc.count, v.ld_mom, MUON_FP32);
+            for (int i = 0; i < pc.count; ++i) {
+              gs.src[pc.slot + i] = src[i];
+              gs.mom[pc.slot + i] = mom[i];
+              gs.ld_src[pc.slot + i] = (int)v.ld_src;
+              gs.ld_mom[pc.slot + i] = (int)v.ld_mom;
+              gs.kind[pc.slot + i] = (unsigned char)(v.src_dtype | (vec ? 4 : 0));
+            }
+            bytes += (double)v.rows * v.cols * pc.count * (dtype_size(v.src_dtype) + 8 + 2 * dtype_size(v.dst_dtype));
+          }
+          const BlockChainArgs ba{L.n, L.m, chunk, ns->iters, prescale ? 0 : 1, cdt, mu, ns->eps, nesterov, ns->coeffs, B.err};
+          ProfScope ps(kProfBlockChain, flops_of(L.n, L.m, ns) * chunk, bytes, s);
+          if (launch_ns_block(ba, gs, us, s) != 0) return MUON_ERR_CUDA;
         } else if (run_chain_launch(ctx, L, B, chunk, ns, prescale, &xi, &out_dt, &us) != 0) {
           return MUON_ERR_CUDA;
         }

@@ -153,19 +153,25 @@ constexpr size_t kFusedSmallMaxSmem = 200 * 1024;
 size_t fused_small_smem(int n, int m, int mode);
 int launch_fused_small(const FusedSmallArgs& a, cudaStream_t s);
 
-// Whole 16-bit standard chain and update of blocks with n <= 128 in one launch
-// (ns_block.cu).
+// Whole step of blocks with n <= 128 in one launch: momentum, norm, 16-bit
+// standard chain and update (ns_block.cu).
 constexpr int kBlockChainMaxIters = 64;
+struct PackSlots {
+  const void* src[UpdateSlots::kMax];         // G of batch index b
+  float* mom[UpdateSlots::kMax];              // M
+  int ld_src[UpdateSlots::kMax], ld_mom[UpdateSlots::kMax];
+  unsigned char kind[UpdateSlots::kMax];      // bits 0-1: G dtype; bit 2: rows of G and M start on 16 bytes
+};
 struct BlockChainArgs {
-  int n, m, count, iters, raw;
+  int n, m, count, iters, raw;      // raw: X holds U and the chain applies the norm
   int dtype;                        // the chain's type
-  const void* x; int ld_x; long long x_bs;
-  const float* inv;
+  float mu, eps;
+  int nesterov;
   const float* coeffs;              // host, 3 * iters
   int* err;
 };
 bool ns_block_ok(int n, int m, int iters);
-int launch_ns_block(const BlockChainArgs& a, const UpdateSlots& u, cudaStream_t s);
+int launch_ns_block(const BlockChainArgs& a, const PackSlots& g, const UpdateSlots& u, cudaStream_t s);
 
 // Per-device caches cover device ordinals below kMaxDevices.
 constexpr int kMaxDevices = 64;

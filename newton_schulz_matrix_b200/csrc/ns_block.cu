@@ -1,7 +1,8 @@
-// The whole Newton-Schulz chain and update of small blocks in one launch: n <= 128
-// rows (the heads of an attention projection), up to 4096 columns, 16-bit
-// storage, the standard form.
+// The whole Muon step of small blocks in one launch: n <= 128 rows (the heads of an
+// attention projection), up to 4096 columns, 16-bit storage, the standard form.
 //
+//   M <- mu M + (1 - mu) G,  U = M or (1 - mu) G + mu M
+//   X = U / (||U|| + eps)
 //   A = f^2 X X^T,  B = b A + c A A,  X <- f (a X + B X)   K times,
 //   then W <- decay W - step X
 //
@@ -17,6 +18,12 @@
 // swizzle.  The same bytes are both operands of X X^T (rows contiguous along
 // the sum) and the B operand of B X (columns contiguous, rows along the sum), so
 // nothing is transposed.
+//   U       each warp turns 32 x 32 boxes of its CTA's slice; G and M come by
+//           asynchronous copies, half a box ahead, through the memory that X
+//           takes later.  U waits in TMEM, in fp32, until the cluster has added
+//           up its squares, so G and M are read once although X is rounded only
+//           after the norm is known (a pass for the norm and one that stores X
+//           read both twice: 52 of the 183 us that the step below then took)
 //   X X^T   each CTA sums its slice's columns into TMEM; the partial sums (fp32)
 //           go to shared memory, CTA r adds rows [128 r / C, 128 (r + 1) / C) of
 //           all CTAs over distributed shared memory in rank order, and stores
@@ -32,7 +39,9 @@
 // Bounded by latency: of the 16 thousand cycles of an iteration (four CTAs, 512
 // columns each) the tensor cores work 4.6; X X^T takes 3.0 thousand, the sum over
 // the CTAs and its barriers 6.8, B 1.6, B X and its epilogue 4.6.  64 blocks of
-// 128 x 2048 take 118 us in two waves of 37 clusters.
+// 128 x 2048 take 156 us in two waves of 37 clusters, of which U is about 35 (HBM:
+// 26 for G, M and the new M).  Pushing the partial sums to the CTA that adds them
+// instead of reading them from there: 159 us, 166 with 16-byte stores to rows.
 //
 // Waits on mbarriers are bounded; on expiry a CTA raises its abort flag, skips
 // its further waits and still takes part in every cluster barrier, so that none
@@ -48,7 +57,7 @@ namespace tc {
 namespace blk {
 
 constexpr int EPI_WARPS = 16;
-constexpr int THREADS = 32 * EPI_WARPS + 32;         // and one warp that issues the loads and MMAs
+constexpr int THREADS = 32 * EPI_WARPS + 32;         // and one warp that issues the MMAs
 constexpr int ROWS = 128;
 constexpr int BLOCK_BYTES = ROWS * 128;              // 128 rows x 64 columns
 constexpr int MOST_SLICE = 512;
@@ -60,7 +69,8 @@ static_assert(SMEM <= 232448 && EPI_WARPS * STAGE_TILE_BYTES <= PART_BYTES, "sha
 
 struct BParams {
   int n, m, slice, iters, raw;
-  const float* inv;
+  float mu, eps;
+  int nesterov;
   int* err;
   long long timeout_ns;
   float coeffs[3 * kBlockChainMaxIters];
@@ -114,6 +124,117 @@ __device__ __forceinline__ void blend32(uint8_t* block, int row, int chunk, cons
   }
 }
 
+__device__ __forceinline__ double ld_cluster_f64(uint32_t addr) {
+  double v;
+  asm volatile("ld.shared::cluster.f64 %0, [%1];" : "=d"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]),
+      "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
+      "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(taddr)
+      : "memory");
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void cp_async(uint32_t to, const void* from, int bytes) {
+  if (bytes == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+  else asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(to), "l"(from) : "memory");
+}
+
+// The momentum of one block as its warps see it: 32 x 32 boxes of G and M in W's
+// orientation, two halves of 16 rows each.  Lane l takes rows 4 i + l / 8 of a
+// half and the 4 columns from 4 (l % 8), i = 0..3.
+struct Momentum {
+  const char* src;
+  float* mom;
+  long long ld_g, ld_m;
+  int dt, es;
+  bool vec, turned;
+  uint8_t* ring;   // this warp's 8 KB: half h of M at 2048 h, of G at 4096 + 2048 h
+  uint8_t* stage;  // and 4 KB for a box of U
+};
+struct MBox {
+  long long row, col;  // in W's orientation
+  int rows, cols;      // that exist
+};
+__device__ __forceinline__ MBox mbox(const Momentum& t, const BParams& p, int r0, int gc) {
+  return t.turned ? MBox{gc, r0, p.m - gc, p.n - r0} : MBox{r0, gc, p.n - r0, p.m - gc};
+}
+__device__ __forceinline__ int columns_of(const MBox& x, int r, int c) { return r < x.rows ? min(x.cols - c, 4) : 0; }
+// Starts the copies of a half; what cannot be copied in whole 16-byte pieces is
+// loaded when it is used.
+__device__ __forceinline__ void fetch_half(const Momentum& t, const MBox& x, int h, int lane) {
+  const int c = 4 * (lane & 7);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = h * 16 + 4 * i + (lane >> 3);
+    if (t.vec && columns_of(x, r, c) == 4) {
+      const uint32_t at = smem_u32(t.ring) + 2048 * h + (32 * i + lane) * 16;
+      cp_async(at, t.mom + (x.row + r) * t.ld_m + x.col + c, 16);
+      const char* g = t.src + ((x.row + r) * t.ld_g + x.col + c) * t.es;
+      if (t.es == 4) cp_async(at + 4096, g, 16);
+      else cp_async(smem_u32(t.ring) + 4096 + 2048 * h + (32 * i + lane) * 8, g, 8);
+    }
+  }
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+// M <- mu M + (1 - mu) G of a half, stored; U left in the staging box (row r, 16-byte
+// chunk k at r * 128 + ((k ^ (r & 7)) << 4)).  Returns this lane's sum of squares.
+// A lane reads only what it copied itself, so no other lane is waited for.
+__device__ __forceinline__ float momentum_half(const Momentum& t, const MBox& x, const BParams& p, int h, int lane) {
+  const int c = 4 * (lane & 7);
+  float ssq = 0.f;
+  asm volatile("cp.async.wait_group 1;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = h * 16 + 4 * i + (lane >> 3);
+    const int valid = columns_of(x, r, c);
+    float* at = t.mom + (x.row + r) * t.ld_m + x.col + c;
+    float gs[4], ms[4], us[4];
+    if (t.vec && valid == 4) {
+      const uint8_t* from = t.ring + 2048 * h + (32 * i + lane) * 16;
+      const float4 m = *reinterpret_cast<const float4*>(from);
+      ms[0] = m.x; ms[1] = m.y; ms[2] = m.z; ms[3] = m.w;
+      if (t.es == 4) {
+        const float4 g = *reinterpret_cast<const float4*>(from + 4096);
+        gs[0] = g.x; gs[1] = g.y; gs[2] = g.z; gs[3] = g.w;
+      } else {
+        const uint2 w = *reinterpret_cast<const uint2*>(t.ring + 4096 + 2048 * h + (32 * i + lane) * 8);
+        const float2 lo = t.dt == kBF16 ? unpack2<1>(w.x) : unpack2<0>(w.x);
+        const float2 hi = t.dt == kBF16 ? unpack2<1>(w.y) : unpack2<0>(w.y);
+        gs[0] = lo.x; gs[1] = lo.y; gs[2] = hi.x; gs[3] = hi.y;
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        gs[e] = e < valid ? load_any(t.src, (x.row + r) * t.ld_g + x.col + c + e, t.dt) : 0.f;
+        ms[e] = e < valid ? at[e] : 0.f;
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      ms[e] = p.mu * ms[e] + (1.f - p.mu) * gs[e];
+      us[e] = p.nesterov ? (1.f - p.mu) * gs[e] + p.mu * ms[e] : ms[e];
+      ssq += us[e] * us[e];
+    }
+    if (t.vec && valid == 4) {
+      *reinterpret_cast<float4*>(at) = make_float4(ms[0], ms[1], ms[2], ms[3]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (e < valid) at[e] = ms[e];
+    }
+    *reinterpret_cast<float4*>(t.stage + r * 128 + (((lane & 7) ^ (r & 7)) << 4)) = make_float4(us[0], us[1], us[2], us[3]);
+  }
+  return ssq;
+}
+
 // What a warp needs of one 32 x 32 box of O for the update: where the box lies in
 // W (in W's own orientation), and W's segments, loaded ahead.
 struct Box {
@@ -155,7 +276,7 @@ __device__ __forceinline__ void load_box(Box& x, unsigned kind, int lane) {
 
 template <int IN_FMT, int CL>
 __global__ void __launch_bounds__(THREADS, 1)
-ns_block_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ BParams p,
+ns_block_kernel(const __grid_constant__ BParams p, const __grid_constant__ PackSlots g,
                 const __grid_constant__ UpdateSlots u) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -163,15 +284,14 @@ ns_block_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constan
   uint8_t* A = X + X_BYTES;
   uint8_t* part = A + GRAM_BYTES;
   uint64_t* bars = reinterpret_cast<uint64_t*>(part + PART_BYTES);
-  uint64_t* load_bar = bars;       // X has arrived
-  uint64_t* gram_bar = bars + 1;   // X X^T
-  uint64_t* sq_bar = bars + 2;     // A A
-  uint64_t* up_bar = bars + 3;     // [4] B X, 128 columns each
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 7);
+  uint64_t* gram_bar = bars;       // X X^T
+  uint64_t* sq_bar = bars + 1;     // A A
+  uint64_t* up_bar = bars + 2;     // [4] B X, 128 columns each
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 6);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const bool issuer = warp == EPI_WARPS;     // the warp that issues loads and MMAs
+  const bool issuer = warp == EPI_WARPS;     // the warp that issues the MMAs
   const int q = warp & 3, quarter = warp >> 2;  // TMEM lane quarter; which 32 of 128 columns
   const int row = q * 32 + lane;
   const uint32_t rank = cluster_rank();
@@ -180,7 +300,7 @@ ns_block_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constan
   const int blocks = p.slice / 64, chunks = p.slice / 128;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < 7; ++i) mbar_init(smem_u32(&bars[i]), 1);
+    for (int i = 0; i < 6; ++i) mbar_init(smem_u32(&bars[i]), 1);
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -209,40 +329,111 @@ ns_block_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constan
     return smem_desc(smem_u32(A + (k >> 2) * BLOCK_BYTES) + (k & 3) * (UMMA_K * 2), 16, 1024);
   };
 
+  float inv;  // 1 / (||U|| + eps)
   const unsigned kind = u.kind[b];
   const int boxes = ((p.n + 31) >> 5) * (p.slice / 32);
-  if (issuer) {
-    if (lane == 0) {
-      // columns past m and rows past n arrive as zeros
-      mbar_expect_tx(smem_u32(load_bar), blocks * BLOCK_BYTES);
-      for (int k = 0; k < blocks; ++k)
-        tma_load_3d(smem_u32(X + k * BLOCK_BYTES), &tmap_x, smem_u32(load_bar), col0 + k * 64, 0, b);
-      // this CTA's own copies: waited for whatever the other roles met
-      volatile int never = 0;
-      if (!mbar_wait(smem_u32(load_bar), 0, &never, p.timeout_ns)) *abort_flag = 1;
+
+  // ---- M <- mu M + (1 - mu) G, X = U / (||U|| + eps) (or U, for a chain that takes
+  // the norm as f).  U waits in TMEM, in fp32, for the norm: 128 rows x 512 columns
+  // are exactly all of it, and the chain has not begun.
+  {
+    double* sums = reinterpret_cast<double*>(A);  // per warp, then this CTA's
+    const int width = p.slice / 4;                // columns of this warp
+    if (!issuer) {
+      const unsigned gk = g.kind[b];
+      const Momentum t{reinterpret_cast<const char*>(g.src[b]), g.mom[b], g.ld_src[b], g.ld_mom[b], (int)gk & 3,
+                       (gk & 3) == kFP32 ? 4 : 2, (gk & 4u) != 0, (kind & 1u) != 0, X + warp * 8192, part + warp * 4096};
+      const uint8_t* S = t.stage;
+      const int first = quarter * width, past = first + width;
+      float ssq = 0.f;
+      MBox now = mbox(t, p, q * 32, col0 + first);
+      fetch_half(t, now, 0, lane);
+      fetch_half(t, now, 1, lane);
+#pragma unroll 1
+      for (int c0 = first; c0 < past; c0 += 32) {
+        // the next box's halves are on their way as soon as this one's have been read
+        MBox next = mbox(t, p, q * 32, col0 + c0 + 32);
+        if (c0 + 32 >= past) next.rows = 0;
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {
+          ssq += momentum_half(t, now, p, h, lane);
+          fetch_half(t, next, h, lane);
+        }
+        now = next;
+        __syncwarp();
+        uint32_t v[32];
+        if (t.turned) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            v[i] = *reinterpret_cast<const uint32_t*>(S + i * 128 + (((lane >> 2) ^ (i & 7)) << 4) + (lane & 3) * 4);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const uint4 w = *reinterpret_cast<const uint4*>(S + lane * 128 + ((i ^ (lane & 7)) << 4));
+            v[4 * i] = w.x; v[4 * i + 1] = w.y; v[4 * i + 2] = w.z; v[4 * i + 3] = w.w;
+          }
+        }
+        tmem_st32(tmem + lanes + c0, v);
+        __syncwarp();
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) ssq += __shfl_down_sync(0xffffffffu, ssq, o);
+      if (lane == 0) sums[warp] = (double)ssq;
+      // W is read at the end: bring it into L2 under the iterations
+      for (int k = warp; k < boxes; k += EPI_WARPS) {
+        Box x;
+        locate(x, p, u, b, col0, k);
+        const int es = ((kind >> 1) & 3) == kFP32 ? 4 : 2;
+        if (lane < x.rows && x.cols > 0)
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(x.base + lane * x.ld * es));
+      }
     }
-    __syncwarp();
-  } else {
-    // W is read at the end: bring it into L2 under the iterations
-    for (int k = warp; k < boxes; k += EPI_WARPS) {
-      Box x;
-      locate(x, p, u, b, col0, k);
-      const int es = ((kind >> 1) & 3) == kFP32 ? 4 : 2;
-      if (lane < x.rows && x.cols > 0)
-        asm volatile("prefetch.global.L2 [%0];" ::"l"(x.base + lane * x.ld * es));
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      double t = 0.0;
+      for (int i = 0; i < EPI_WARPS; ++i) t += sums[i];
+      sums[EPI_WARPS] = t;
     }
-    wait(load_bar, 0);
+    if constexpr (CL > 1) cluster_sync();
+    else __syncthreads();
+    double total = 0.0;
+#pragma unroll
+    for (int c = 0; c < CL; ++c)
+      total += CL > 1 ? ld_cluster_f64(mapa(smem_u32(sums + EPI_WARPS), c)) : sums[EPI_WARPS];
+    inv = (float)(1.0 / (sqrt(total) + (double)p.eps));
+    if (!issuer) {
+      const float scale = p.raw ? 1.f : inv;
+#pragma unroll 1
+      for (int c0 = quarter * width; c0 < (quarter + 1) * width; c0 += 32) {
+        uint32_t r[32];
+        tmem_ld32(tmem + lanes + c0, r);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint32_t w[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            w[k] = pack2<IN_FMT>(scale * __uint_as_float(r[8 * i + 2 * k]), scale * __uint_as_float(r[8 * i + 2 * k + 1]));
+          *reinterpret_cast<uint4*>(X + (c0 >> 6) * BLOCK_BYTES + at16(row, ((c0 & 63) >> 3) + i)) =
+              make_uint4(w[0], w[1], w[2], w[3]);
+        }
+      }
+      fence_async_smem();
+      tc_fence_before();
+    }
+    __syncthreads();
+    tc_fence_after();
   }
 
   uint32_t sq_parity = 0;  // of the next A A: iterations without that term skip it
   for (int it = 0; it < p.iters; ++it) {
     const uint32_t parity = it & 1;
     const float a = p.coeffs[3 * it], bb = p.coeffs[3 * it + 1], cc = p.coeffs[3 * it + 2];
-    const float f = it == 0 && p.raw ? p.inv[b] : 1.f;
+    const float f = it == 0 && p.raw ? inv : 1.f;
 
     // ---- A = f^2 X X^T
     if (issuer) {
       if (lane == 0) {
+        fence_async_smem();
         for (int k = 0; k < blocks * 4; ++k) {
           const uint64_t d = smem_desc(smem_u32(X + (k >> 2) * BLOCK_BYTES) + (k & 3) * (UMMA_K * 2), 16, 1024);
           tc_mma(tmem, d, d, idesc_kk, k > 0);
@@ -435,7 +626,7 @@ static int cluster_for(int m) {
 }
 
 template <int IN_FMT, int CL>
-static int launch(const CUtensorMap& map, const BParams& p, const UpdateSlots& u, int count, cudaStream_t s) {
+static int launch(const BParams& p, const PackSlots& g, const UpdateSlots& u, int count, cudaStream_t s) {
   static std::atomic<int> opted[kMaxDevices];
   const int dev = current_device();
   if (dev < 0) return (int)cudaErrorInvalidDevice;
@@ -459,7 +650,7 @@ static int launch(const CUtensorMap& map, const BParams& p, const UpdateSlots& u
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = programmatic_launch() ? 2 : 1;
-  return (int)cudaLaunchKernelEx(&cfg, kern, map, p, u);
+  return (int)cudaLaunchKernelEx(&cfg, kern, p, g, u);
 }
 
 }  // namespace blk
@@ -469,24 +660,22 @@ bool ns_block_ok(int n, int m, int iters) {
   return n <= tc::blk::ROWS && m <= 8 * tc::blk::MOST_SLICE && iters <= kBlockChainMaxIters;
 }
 
-int launch_ns_block(const BlockChainArgs& a, const UpdateSlots& u, cudaStream_t s) {
+int launch_ns_block(const BlockChainArgs& a, const PackSlots& g, const UpdateSlots& u, cudaStream_t s) {
   using namespace tc;
   using namespace tc::blk;
   BParams p{};
   p.n = a.n; p.m = a.m; p.iters = a.iters; p.raw = a.raw;
   const int cluster = cluster_for(a.m);
   p.slice = ((a.m + cluster - 1) / cluster + 127) / 128 * 128;
-  p.inv = a.inv; p.err = a.err;
+  p.mu = a.mu; p.eps = a.eps; p.nesterov = a.nesterov; p.err = a.err;
   p.timeout_ns = wait_timeout_ns();
   for (int i = 0; i < 3 * a.iters; ++i) p.coeffs[i] = a.coeffs[i];
-  CUtensorMap map;
-  if (!encode_map(&map, a.dtype, a.x, a.m, a.n, a.count, a.ld_x, a.x_bs, 64, ROWS)) return (int)cudaErrorInvalidValue;
   const bool bf = a.dtype == kBF16;
   switch (cluster) {
-    case 1: return bf ? launch<1, 1>(map, p, u, a.count, s) : launch<0, 1>(map, p, u, a.count, s);
-    case 2: return bf ? launch<1, 2>(map, p, u, a.count, s) : launch<0, 2>(map, p, u, a.count, s);
-    case 4: return bf ? launch<1, 4>(map, p, u, a.count, s) : launch<0, 4>(map, p, u, a.count, s);
-    default: return bf ? launch<1, 8>(map, p, u, a.count, s) : launch<0, 8>(map, p, u, a.count, s);
+    case 1: return bf ? launch<1, 1>(p, g, u, a.count, s) : launch<0, 1>(p, g, u, a.count, s);
+    case 2: return bf ? launch<1, 2>(p, g, u, a.count, s) : launch<0, 2>(p, g, u, a.count, s);
+    case 4: return bf ? launch<1, 4>(p, g, u, a.count, s) : launch<0, 4>(p, g, u, a.count, s);
+    default: return bf ? launch<1, 8>(p, g, u, a.count, s) : launch<0, 8>(p, g, u, a.count, s);
   }
 }
 

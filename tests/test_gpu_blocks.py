@@ -226,3 +226,41 @@ def test_more_small_blocks_than_one_launch_takes():
     nsm.muon_step_blocks([w], [g], [m], [None])
     nsm.muon_step_blocks([w2], [g], [m2], [None], workspace=torch.empty(20 * lo, dtype=torch.uint8, device="cuda"))
     assert torch.equal(w, w2) and torch.equal(m, m2)
+
+
+@pytest.mark.parametrize("chain", ["fp16", "bf16"])
+@pytest.mark.parametrize("block", [(64, 640), (640, 64), (33, 517), (517, 33), (128, 2049), (31, 95), (1, 1)])
+def test_small_blocks_momentum_of_every_type_and_pitch(block, chain):
+    """One launch reads G and M itself: G's types, pitches and alignments, both orientations and no Nesterov
+    step give muon_step's momentum bit for bit and the oracle's weights; nothing else in the storages moves."""
+    for i, (gdt, view, nesterov) in enumerate((("bf16", None, True), ("fp16", "wide", False), ("fp32", "odd", True),
+                                               ("fp32", None, False), ("fp16", "odd", True))):
+        shape = (2, block[0], 2 * block[1])
+        (w, _), (g, _), (m, ms) = (make(shape, view, dt, 90 + 3 * i + k, s) for k, (dt, s) in enumerate(
+            ((torch.float32, 0.05), (TYPES[gdt], 1.0), (torch.float32, 0.2))))
+        wd, gd, md = (cut(t, block) for t in (w, g, m))
+        old = [[t.double().cpu() for t in ts] for ts in (wd, gd)]
+        hp = dict(nesterov=nesterov, compute_dtype=chain)
+        nsm.muon_step(wd, gd, md, **hp)
+        status = torch.full((4,), -1, dtype=torch.int32, device="cuda")
+        nsm.muon_step_blocks([w], [g], [m], [block], status=status, **hp)
+        assert status.tolist() == [0] * 4
+        for got, want in zip(cut(m, block), md):
+            assert torch.equal(got, want)
+        for got, w0, g0, m1 in zip(cut(w, block), *old, md):
+            m1 = m1.double().cpu()
+            check_weights(got, w0, 0.05 * g0 + 0.95 * m1 if nesterov else m1, block, chain)
+        m.fill_(7.0)
+        assert bool((ms == 7).all())
+
+
+def test_small_blocks_of_several_kinds_in_one_launch():
+    """Blocks of one orientation share a launch, each with its own gradient type, pitch and orientation."""
+    specs = [((2, 64, 320), "bf16", None), ((320, 64), "fp16", "wide"), ((64, 320), "fp32", "odd"), ((320, 64), "bf16", "odd")]
+    ws, gs, ms = ([make(s, v, (torch.bfloat16, TYPES[d], torch.float32)[k], 120 + 3 * i + k, (0.05, 1.0, 0.2)[k])[0]
+                   for i, (s, d, v) in enumerate(specs)] for k in range(3))
+    one = [[t.clone() for t in ts] for ts in (ws, gs, ms)]
+    nsm.muon_step_blocks(ws, gs, ms, [None] * 4)
+    for i in range(4):
+        nsm.muon_step_blocks([one[0][i]], [one[1][i]], [one[2][i]], [None])
+        assert torch.equal(ws[i], one[0][i]) and torch.equal(ms[i], one[2][i])
