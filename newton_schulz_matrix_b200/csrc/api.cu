@@ -630,7 +630,17 @@ int run_batches(const std::vector<Batch>& batches, const std::vector<GroupView>&
     // small blocks run their whole chain and update in one launch (muon_step keeps the separate products)
     const bool one_launch = update && blocks && ns->compute_dtype != MUON_FP32 && ns->mode == MUON_NS_STANDARD &&
                             ns_block_ok(L.n, L.m, ns->iters);
-    const bool fuse = one_launch || (update && ns->compute_dtype != MUON_FP32 && fused_update_enabled() && gemm_tc_paired(L.n));
+    // W whose rows start on 16 bytes is written by the last product, other W by the
+    // separate update, whose warps access it by columns.  Steps of one iteration on 4
+    // matrices: 1300 x 1300 blocks that start on 8 bytes 334 us by the product, 236 by
+    // the update; 1408 x 2048 on 16 bytes 160 and 166.
+    bool rows_ok = true;
+    for (const Seg& sg : bt.segs) {
+      const GroupView& v = views[sg.group];
+      rows_ok = rows_ok && (!update || rows16(v.dst + sg.first, sg.count, v.ld_dst, v.dst_dtype));
+    }
+    const bool fuse = one_launch || (update && rows_ok && ns->compute_dtype != MUON_FP32 && fused_update_enabled() &&
+                                     gemm_tc_paired(L.n));
     int chunk_cap = (int)std::min<size_t>((size_t)bt.total, (ws_bytes - L.fixed) / L.per_matrix);
     if (fuse) chunk_cap = std::min(chunk_cap, UpdateSlots::kMax);
     // slots are assigned in segment order; walk them chunk by chunk

@@ -148,7 +148,8 @@ pack_kernel(const PackArgs a, const __grid_constant__ SegmentPtrs p) {
   float* mom = MOMENTUM ? p.mom[b] : nullptr;
   TX* x = reinterpret_cast<TX*>(a.x) + (long long)b * a.x_batch_stride;
 
-  const bool full = (r0 + kTile <= a.rows) && (c0 + kTile <= a.cols) && a.vec;
+  const bool inside = r0 + kTile <= a.rows && c0 + kTile <= a.cols;  // x's rows start on 16 bytes
+  const bool full = inside && a.vec;
   const bool store = a.pass != 1;
   float u[4][4];  // [row pass][element]
   if (full) {
@@ -175,23 +176,34 @@ pack_kernel(const PackArgs a, const __grid_constant__ SegmentPtrs p) {
       }
     }
   } else {
+    // the same elements per thread, and again every load before the first store
+    // (rows that start anywhere, and ragged tiles)
+    float g[4][4], m[4][4];
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      const int r = r0 + q * 16 + lr;
+      const long long r = r0 + q * 16 + lr;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int c = c0 + lc + i;
-        u[q][i] = 0.f;
-        if (r < a.rows && c < a.cols) {
-          const float gv = to_f32(src[(long long)r * a.ld_src + c]);
-          if (MOMENTUM) {
-            const long long off = (long long)r * a.ld_mom + c;
-            const float mv = a.mu * mom[off] + (1.f - a.mu) * gv;
-            if (store) mom[off] = mv;
-            u[q][i] = a.nesterov ? (1.f - a.mu) * gv + a.mu * mv : mv;
-          } else {
-            u[q][i] = gv;
-          }
+        const bool in = r < a.rows && c < a.cols;
+        g[q][i] = in ? to_f32(src[r * a.ld_src + c]) : 0.f;
+        if (MOMENTUM) m[q][i] = in ? mom[r * a.ld_mom + c] : 0.f;
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const long long r = r0 + q * 16 + lr;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int c = c0 + lc + i;
+        if (!(r < a.rows && c < a.cols)) {
+          u[q][i] = 0.f;
+        } else if (MOMENTUM) {
+          const float mv = a.mu * m[q][i] + (1.f - a.mu) * g[q][i];
+          if (store) mom[r * a.ld_mom + c] = mv;
+          u[q][i] = a.nesterov ? (1.f - a.mu) * g[q][i] + a.mu * mv : mv;
+        } else {
+          u[q][i] = g[q][i];
         }
       }
     }
@@ -221,7 +233,7 @@ pack_kernel(const PackArgs a, const __grid_constant__ SegmentPtrs p) {
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       const int r = r0 + q * 16 + lr;
-      if (full) {
+      if (inside) {
         store4(x + (long long)r * a.ld_x + c0 + lc, u[q]);
       } else if (r < a.rows) {
 #pragma unroll
@@ -236,14 +248,13 @@ pack_kernel(const PackArgs a, const __grid_constant__ SegmentPtrs p) {
       for (int i = 0; i < 4; ++i) tile[q * 16 + lr][lc + i] = u[q][i];
     __syncthreads();
     // oriented row j = storage column c0 + q * 16 + lr; oriented columns = storage rows r0 + lc + i
-    const bool fullT = (c0 + kTile <= a.cols) && (r0 + kTile <= a.rows);
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       const int j = c0 + q * 16 + lr;
       float v[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) v[i] = tile[lc + i][q * 16 + lr];
-      if (fullT) {
+      if (inside) {
         store4(x + (long long)j * a.ld_x + r0 + lc, v);
       } else if (j < a.cols) {
 #pragma unroll
@@ -291,7 +302,8 @@ unpack_kernel(const UnpackArgs a, const __grid_constant__ SegmentPtrs p) {
   const int lr = threadIdx.x >> 2, lc = (threadIdx.x & 3) * 16;
   const TX* __restrict__ x = reinterpret_cast<const TX*>(a.x) + (long long)b * a.x_batch_stride;
   TD* __restrict__ dst = reinterpret_cast<TD*>(p.dst[b]);
-  const bool full = (r0 + kTile <= a.rows) && (c0 + kTile <= a.cols) && a.vec;
+  const bool inside = r0 + kTile <= a.rows && c0 + kTile <= a.cols;  // x's rows start on 16 bytes
+  const bool full = inside && a.vec;
   const int r = r0 + lr;
   const long long off = (long long)r * a.ld_dst + c0 + lc;
 
@@ -299,6 +311,16 @@ unpack_kernel(const UnpackArgs a, const __grid_constant__ SegmentPtrs p) {
   // so each thread waits for one memory round trip, not two.
   float w[16];
   if (UPDATE && full) load16(dst + off, w);
+  // W's rows may start anywhere: a thread then takes every fourth row of one
+  // column, so that a warp's accesses are consecutive (sixteen elements of a row
+  // per thread, each loaded, updated and stored in turn, made a step of
+  // 4097 x 4099 of one iteration 730 us long, not 430)
+  const int ec = c0 + (threadIdx.x & 63), er = r0 + (threadIdx.x >> 6);
+  if (UPDATE && !full) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      w[i] = er + 4 * i < a.rows && ec < a.cols ? to_f32(dst[(er + 4 * i) * a.ld_dst + ec]) : 0.f;
+  }
   float o[16];
   if (!TRANS) {
     if (full) {
@@ -306,13 +328,13 @@ unpack_kernel(const UnpackArgs a, const __grid_constant__ SegmentPtrs p) {
     } else {
 #pragma unroll
       for (int i = 0; i < 16; ++i)
-        o[i] = (r < a.rows && c0 + lc + i < a.cols) ? to_f32(x[(long long)r * a.ld_x + c0 + lc + i]) : 0.f;
+        o[i] = er + 4 * i < a.rows && ec < a.cols ? to_f32(x[(long long)(er + 4 * i) * a.ld_x + ec]) : 0.f;
     }
   } else {
     // read oriented rows j = c0 + lr (storage columns), oriented cols = storage rows
     const int j = c0 + lr;
     float v[16];
-    if (full) {
+    if (inside) {
       load16(x + (long long)j * a.ld_x + r0 + lc, v);
     } else {
 #pragma unroll
@@ -323,7 +345,7 @@ unpack_kernel(const UnpackArgs a, const __grid_constant__ SegmentPtrs p) {
     for (int i = 0; i < 16; ++i) tile[lr][lc + i] = v[i];
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < 16; ++i) o[i] = tile[lc + i][lr];
+    for (int i = 0; i < 16; ++i) o[i] = full ? tile[lc + i][lr] : tile[threadIdx.x & 63][(threadIdx.x >> 6) + 4 * i];
   }
 
   if (full) {
@@ -335,16 +357,11 @@ unpack_kernel(const UnpackArgs a, const __grid_constant__ SegmentPtrs p) {
       for (int i = 0; i < 16; ++i) w[i] = o[i];
     }
     store16(dst + off, w);
-  } else if (r < a.rows) {
+  } else {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const int c = c0 + lc + i;
-      if (c < a.cols) {
-        const long long o2 = (long long)r * a.ld_dst + c;
-        float v = UPDATE ? weight_update(to_f32(dst[o2]), o[i], a.decay, a.step) : o[i];
-        dst[o2] = from_f32<TD>(v);
-      }
-    }
+    for (int i = 0; i < 16; ++i)
+      if (er + 4 * i < a.rows && ec < a.cols)
+        dst[(er + 4 * i) * a.ld_dst + ec] = from_f32<TD>(UPDATE ? weight_update(w[i], o[i], a.decay, a.step) : o[i]);
   }
 
   if (a.status != nullptr) {
