@@ -42,6 +42,8 @@
 // 128 x 2048 take 156 us in two waves of 37 clusters, of which U is about 35 (HBM:
 // 26 for G, M and the new M).  Pushing the partial sums to the CTA that adds them
 // instead of reading them from there: 159 us, 166 with 16-byte stores to rows.
+// Blocks whose rows start anywhere load element by element, whole pieces at a time:
+// 64 of 127 x 2047 take 225 us (297 with one load after the other).
 //
 // Waits on mbarriers are bounded; on expiry a CTA raises its abort flag, skips
 // its further waits and still takes part in every cluster barrier, so that none
@@ -106,6 +108,22 @@ __device__ __forceinline__ float2 unpack2(uint32_t w) {
   if (IN_FMT) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
   return __half22float2(*reinterpret_cast<const __half2*>(&w));
 }
+// Up to `count` elements of es bytes, `stride` bytes apart, as bits: the type is
+// looked at once, so that all the loads are in flight together.
+template <int N>
+__device__ __forceinline__ void load_bits(uint32_t (&v)[N], const char* p, long long stride, int count, int es) {
+  if (es == 4) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = i < count ? *reinterpret_cast<const uint32_t*>(p + i * stride) : 0u;
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = i < count ? *reinterpret_cast<const uint16_t*>(p + i * stride) : 0u;
+  }
+}
+__device__ __forceinline__ float value_of(uint32_t bits, int dt) {
+  if (dt == kFP32) return __uint_as_float(bits);
+  return dt == kBF16 ? __uint_as_float(bits << 16) : __half2float(__ushort_as_half((unsigned short)bits));
+}
 // Four 16-byte chunks (32 values) of a row: x <- s * acc + c * x, rounded.
 template <int IN_FMT>
 __device__ __forceinline__ void blend32(uint8_t* block, int row, int chunk, const uint32_t (&acc)[32], float s, float c) {
@@ -166,15 +184,17 @@ struct MBox {
 __device__ __forceinline__ MBox mbox(const Momentum& t, const BParams& p, int r0, int gc) {
   return t.turned ? MBox{gc, r0, p.m - gc, p.n - r0} : MBox{r0, gc, p.n - r0, p.m - gc};
 }
-__device__ __forceinline__ int columns_of(const MBox& x, int r, int c) { return r < x.rows ? min(x.cols - c, 4) : 0; }
-// Starts the copies of a half; what cannot be copied in whole 16-byte pieces is
-// loaded when it is used.
+// A half that exists whole, of rows that start on 16 bytes, comes by asynchronous
+// copies; others are loaded when they are used.
+__device__ __forceinline__ bool copied(const Momentum& t, const MBox& x, int h) {
+  return t.vec && x.rows >= h * 16 + 16 && x.cols >= 32;
+}
 __device__ __forceinline__ void fetch_half(const Momentum& t, const MBox& x, int h, int lane) {
-  const int c = 4 * (lane & 7);
+  if (copied(t, x, h)) {
+    const int c = 4 * (lane & 7);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = h * 16 + 4 * i + (lane >> 3);
-    if (t.vec && columns_of(x, r, c) == 4) {
+    for (int i = 0; i < 4; ++i) {
+      const int r = h * 16 + 4 * i + (lane >> 3);
       const uint32_t at = smem_u32(t.ring) + 2048 * h + (32 * i + lane) * 16;
       cp_async(at, t.mom + (x.row + r) * t.ld_m + x.col + c, 16);
       const char* g = t.src + ((x.row + r) * t.ld_g + x.col + c) * t.es;
@@ -184,23 +204,32 @@ __device__ __forceinline__ void fetch_half(const Momentum& t, const MBox& x, int
   }
   asm volatile("cp.async.commit_group;" ::: "memory");
 }
-// M <- mu M + (1 - mu) G of a half, stored; U left in the staging box (row r, 16-byte
-// chunk k at r * 128 + ((k ^ (r & 7)) << 4)).  Returns this lane's sum of squares.
-// A lane reads only what it copied itself, so no other lane is waited for.
+// M <- mu M + (1 - mu) G of four elements: ms and the sum of squares on, U to the staging box.
+__device__ __forceinline__ void momentum4(const BParams& p, const float (&gs)[4], float (&ms)[4], float& ssq, uint8_t* to) {
+  float us[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    ms[e] = p.mu * ms[e] + (1.f - p.mu) * gs[e];
+    us[e] = p.nesterov ? (1.f - p.mu) * gs[e] + p.mu * ms[e] : ms[e];
+    ssq += us[e] * us[e];
+  }
+  *reinterpret_cast<float4*>(to) = make_float4(us[0], us[1], us[2], us[3]);
+}
+// The momentum of a half, stored; U left in the staging box (row r, 16-byte chunk k
+// at r * 128 + ((k ^ (r & 7)) << 4)).  Returns this lane's sum of squares.  A lane
+// reads only what it copied itself, so no other lane is waited for.
 __device__ __forceinline__ float momentum_half(const Momentum& t, const MBox& x, const BParams& p, int h, int lane) {
   const int c = 4 * (lane & 7);
   float ssq = 0.f;
+  auto stage = [&](int r) { return t.stage + r * 128 + (((lane & 7) ^ (r & 7)) << 4); };
   asm volatile("cp.async.wait_group 1;" ::: "memory");
+  if (copied(t, x, h)) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = h * 16 + 4 * i + (lane >> 3);
-    const int valid = columns_of(x, r, c);
-    float* at = t.mom + (x.row + r) * t.ld_m + x.col + c;
-    float gs[4], ms[4], us[4];
-    if (t.vec && valid == 4) {
+    for (int i = 0; i < 4; ++i) {
+      const int r = h * 16 + 4 * i + (lane >> 3);
       const uint8_t* from = t.ring + 2048 * h + (32 * i + lane) * 16;
       const float4 m = *reinterpret_cast<const float4*>(from);
-      ms[0] = m.x; ms[1] = m.y; ms[2] = m.z; ms[3] = m.w;
+      float gs[4], ms[4] = {m.x, m.y, m.z, m.w};
       if (t.es == 4) {
         const float4 g = *reinterpret_cast<const float4*>(from + 4096);
         gs[0] = g.x; gs[1] = g.y; gs[2] = g.z; gs[3] = g.w;
@@ -210,27 +239,37 @@ __device__ __forceinline__ float momentum_half(const Momentum& t, const MBox& x,
         const float2 hi = t.dt == kBF16 ? unpack2<1>(w.y) : unpack2<0>(w.y);
         gs[0] = lo.x; gs[1] = lo.y; gs[2] = hi.x; gs[3] = hi.y;
       }
-    } else {
+      momentum4(p, gs, ms, ssq, stage(r));
+      *reinterpret_cast<float4*>(t.mom + (x.row + r) * t.ld_m + x.col + c) = make_float4(ms[0], ms[1], ms[2], ms[3]);
+    }
+    return ssq;
+  }
+#pragma unroll 1
+  for (int k = 0; k < 4; k += 2) {
+    // eight rows: every load before the first store
+    uint32_t gb[2][4], mb[2][4];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = h * 16 + 4 * (k + i) + (lane >> 3);
+      const int valid = r < x.rows ? min(x.cols - c, 4) : 0;
+      load_bits<4>(gb[i], t.src + ((x.row + r) * t.ld_g + x.col + c) * t.es, t.es, valid, t.es);
+      load_bits<4>(mb[i], reinterpret_cast<const char*>(t.mom + (x.row + r) * t.ld_m + x.col + c), 4, valid, 4);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = h * 16 + 4 * (k + i) + (lane >> 3);
+      float* at = t.mom + (x.row + r) * t.ld_m + x.col + c;
+      float gs[4], ms[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        gs[e] = e < valid ? load_any(t.src, (x.row + r) * t.ld_g + x.col + c + e, t.dt) : 0.f;
-        ms[e] = e < valid ? at[e] : 0.f;
+        gs[e] = value_of(gb[i][e], t.dt);
+        ms[e] = __uint_as_float(mb[i][e]);
       }
-    }
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      ms[e] = p.mu * ms[e] + (1.f - p.mu) * gs[e];
-      us[e] = p.nesterov ? (1.f - p.mu) * gs[e] + p.mu * ms[e] : ms[e];
-      ssq += us[e] * us[e];
-    }
-    if (t.vec && valid == 4) {
-      *reinterpret_cast<float4*>(at) = make_float4(ms[0], ms[1], ms[2], ms[3]);
-    } else {
+      momentum4(p, gs, ms, ssq, stage(r));
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        if (e < valid) at[e] = ms[e];
+        if (r < x.rows && c + e < x.cols) at[e] = ms[e];
     }
-    *reinterpret_cast<float4*>(t.stage + r * 128 + (((lane & 7) ^ (r & 7)) << 4)) = make_float4(us[0], us[1], us[2], us[3]);
   }
   return ssq;
 }
@@ -593,6 +632,25 @@ ns_block_kernel(const __grid_constant__ BParams p, const __grid_constant__ PackS
                        : "memory");
         __syncwarp();
       }
+      if (!(kind & 8u)) {
+        // rows of W that start anywhere: a lane per column, sixteen rows in flight
+#pragma unroll 1
+        for (int r0 = 0; r0 < now.rows; r0 += 16) {
+          uint32_t v[16];
+          load_bits<16>(v, now.base + (r0 * now.ld + lane) * es, now.ld * es, lane < now.cols ? now.rows - r0 : 0, es);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const int r = r0 + e;
+            if (r >= now.rows || lane >= now.cols) continue;
+            const uint16_t* at = reinterpret_cast<const uint16_t*>(
+                (kind & 1u) ? S + sw64(r, lane >> 3) : x + at16(now.r0 + r, ch + (lane >> 3))) + (lane & 7);
+            const float o = load_any(at, 0, IN_FMT ? kBF16 : kFP16);
+            bad |= !isfinite(o);
+            store_any(now.base + r * now.ld * es, lane, wdt, weight_update(value_of(v[e], wdt), o, u.decay, u.step));
+          }
+        }
+        continue;
+      }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int r = i * 8 + (lane >> 2), c = (lane & 3) * 8;
@@ -606,7 +664,7 @@ ns_block_kernel(const __grid_constant__ BParams p, const __grid_constant__ PackS
           else o[e] = __half2float(reinterpret_cast<const __half*>(&seg)[e]);
           bad |= e < valid && !isfinite(o[e]);
         }
-        update8(now.base + (r * now.ld + c) * es, wdt, o, valid, valid == 8 && (kind & 8u), u.decay, u.step,
+        update8(now.base + (r * now.ld + c) * es, wdt, o, valid, valid == 8, u.decay, u.step,
                 box_vec(now, kind, i, lane), now.w[i]);
       }
     }

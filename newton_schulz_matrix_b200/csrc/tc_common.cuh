@@ -451,12 +451,9 @@ __device__ __forceinline__ void update8(char* w, int wdt, const float* o, int va
     }
     *reinterpret_cast<uint4*>(w) = x;
   } else {
-    float x[8];  // every load before the first store: one memory round trip
-#pragma unroll
-    for (int k = 0; k < 8; ++k) x[k] = k < valid ? load_any(w, k, wdt) : 0.f;
 #pragma unroll
     for (int k = 0; k < 8; ++k)
-      if (k < valid) store_any(w, k, wdt, weight_update(x[k], o[k], decay, step));
+      if (k < valid) store_any(w, k, wdt, weight_update(load_any(w, k, wdt), o[k], decay, step));
   }
 }
 
