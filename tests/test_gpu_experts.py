@@ -593,3 +593,27 @@ def test_expert_launches_are_profiled():
     for name in ("expert_sort", "expert_gather", "expert_combine", "expert_combine_backward"):
         assert prof[name]["launches"] == 1 and prof[name]["ms"] > 0, name
     assert sum(r["launches"] for name, r in prof.items() if name.startswith("expert_product")) == 2
+
+
+# ---------------------------------------------------------------- forms of their own
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("rows", [4096, 4097, 16384, 16385])
+def test_long_fp32_weight_gradients_keep_their_accuracy(rows, dtype):
+    """fp32 dW of 16-bit operands at lengths around whole runs of 512 tokens.
+
+    A run is 32 steps of 16 tokens, each of which truncates its sum: at most one
+    step of 2^-23 relative to a partial sum that grows as sqrt(k), half of it on
+    average, times the mean 0.72 of 1 / mantissa.  That is 0.36 * 2^-23 *
+    sum sqrt(k / 32) = 9.4e-7 relative to the result, whatever the number of runs
+    (they are added with round-to-nearest).  One sum over 4096 tokens would have
+    256 steps and 7.3e-6, over 16384 2.9e-5: 1.5e-6 lies between."""
+    counts = [rows, 513]
+    offsets, xs, dys, _ = product_case(25, counts, 256, 264, dtype)
+    dw = nsm.muon_expert_weight_grad(dys, xs, offsets, out_dtype=SF)
+    for e, (lo, hi) in enumerate(segments(offsets, xs.shape[0])):
+        ref = f64(dys[lo:hi]).T @ f64(xs[lo:hi])
+        err = float((f64(dw[e]) - ref).norm() / ref.norm())
+        assert err <= 1.5e-6, (e, err)
+    out = torch.zeros_like(dw)
+    nsm.muon_expert_weight_grad(dys, xs, offsets, out=out, accumulate=True)
+    assert torch.equal(out, dw)
