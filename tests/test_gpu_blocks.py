@@ -264,3 +264,25 @@ def test_small_blocks_of_several_kinds_in_one_launch():
     for i in range(4):
         nsm.muon_step_blocks([one[0][i]], [one[1][i]], [one[2][i]], [None])
         assert torch.equal(ws[i], one[0][i]) and torch.equal(ms[i], one[2][i])
+
+
+@pytest.mark.parametrize("block,hp", [
+    ((128, 4097), {}), ((64, 7168), {}), ((7168, 64), {}), ((128, 7168), {}), ((4100, 33), {"compute_dtype": "bf16"}),
+    ((64, 384), {"coeffs": [oracle.CUBIC] * 65}), ((64, 384), {"mode": "gram"}), ((384, 64), {"mode": "gram_stabilized"}),
+    ((128, 2048), {"mode": "gram_stabilized"}), ((33, 517), {"mode": "gram_stabilized", "restart_every": 1}),
+    ((1, 48), {"mode": "gram"}), ((128, 7168), {"mode": "gram_stabilized"}),
+    ((64, 384), {"mode": "gram", "gram_dtype": "bf16"}), ((100, 96), {"mode": "gram_stabilized", "compute_dtype": "fp32"})])
+def test_small_blocks_that_one_launch_does_not_take(block, hp):
+    """More than 4096 columns, more than 64 iterations, the Gram forms: muon_step's products, bit for bit."""
+    odd = block[1] % 8 != 0
+    (w, ws), (g, _), (m, ms) = (make((2, block[0], 2 * block[1]), "odd" if odd else None, dt, 150 + i, s) for i, (dt, s) in
+                                enumerate(((torch.bfloat16, 0.05), (torch.bfloat16, 1.0), (torch.float32, 0.2))))
+    wd, gd, md = (cut(t, block) for t in (w, g, m))
+    nsm.muon_step(wd, gd, md, **hp)
+    nsm.muon_profile_begin()
+    status = torch.full((4,), -1, dtype=torch.int32, device="cuda")
+    nsm.muon_step_blocks([w], [g], [m], [block], status=status, **hp)
+    assert "ns_block_kernel" not in [r["kernel"] for r in nsm.muon_profile_end()]
+    assert status.tolist() == [0] * 4
+    for got, want in zip(cut(w, block) + cut(m, block), wd + md):
+        assert torch.equal(got, want)

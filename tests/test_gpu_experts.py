@@ -617,3 +617,24 @@ def test_long_fp32_weight_gradients_keep_their_accuracy(rows, dtype):
     out = torch.zeros_like(dw)
     nsm.muon_expert_weight_grad(dys, xs, offsets, out=out, accumulate=True)
     assert torch.equal(out, dw)
+
+
+@pytest.mark.parametrize("dtype", [BF, HF, SF])
+@pytest.mark.parametrize("counts,inner,outer", [([40, 0, 300], 128, 96), ([3, 1, 0, 5], 64, 264)])
+def test_products_of_permuted_stacks(counts, inner, outer, dtype):
+    """Weights and dW whose experts alternate row by row: the expert stride is below the row pitch."""
+    offsets, xs, dys, w = product_case(26, counts, inner, outer, dtype)
+    permuted = w.permute(1, 0, 2).contiguous().permute(1, 0, 2)
+    assert permuted.stride(0) == inner < permuted.stride(1)
+    check_products(offsets, xs, dys, permuted, U_NEAREST if dtype == SF else U_TRUNCATED)
+    used = sum(counts)
+    for call, rows in ((nsm.muon_expert_product, xs), (nsm.muon_expert_input_grad, dys)):
+        assert torch.equal(call(rows, permuted, offsets)[:used], call(rows, w, offsets)[:used])
+    for dw_dtype, accumulate in ((dtype, False), (SF, False), (SF, True)):
+        store = torch.full((outer + 1, len(counts) + 1, inner), 7.0, dtype=dw_dtype, device="cuda")
+        out = store[:outer, :len(counts)].permute(1, 0, 2)
+        dense = torch.full((len(counts), outer, inner), 7.0, dtype=dw_dtype, device="cuda")
+        nsm.muon_expert_weight_grad(dys, xs, offsets, out=out, accumulate=accumulate)
+        nsm.muon_expert_weight_grad(dys, xs, offsets, out=dense, accumulate=accumulate)
+        assert torch.equal(out, dense)
+        assert bool((store[outer:] == 7).all()) and bool((store[:, len(counts):] == 7).all())
