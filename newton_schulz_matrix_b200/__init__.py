@@ -993,6 +993,10 @@ class ExpertMuonStep:
     buffer's type, the operands' (default: each stack's own) or float32.
     ``blocks`` as for muon_step_blocks, one entry per stack.  Calls share the
     buffer and the workspace and must not overlap on the GPU.
+
+    A slice whose weight gradients hit a device-side timeout has stepped on an
+    unfinished buffer: all of its blocks carry MUON_STATUS_TIMEOUT in ``status``,
+    and their weights and momentum are to be restored from before the call.
     """
 
     def __init__(self, params, moms, *, blocks: Sequence | None = None, slice_bytes: int = 512 << 20,
@@ -1027,6 +1031,8 @@ class ExpertMuonStep:
                                      device=self.device)
         for step in self.steps:
             step.workspace = self.workspace
+        # the status word of each slice's weight gradients
+        self.words = torch.zeros(len(self.slices), dtype=torch.int32, device=self.device).split(1)
 
     def __call__(self, factors, stream=None) -> None:
         if len(factors) != len(self.shapes):
@@ -1045,12 +1051,13 @@ class ExpertMuonStep:
         if not _here(self.device, stream):
             return _elsewhere(self.device, stream, self, factors)
         handle = _raw_stream(self.device.index)
-        for (i, e0, e1), grad, step in zip(self.slices, self.grads, self.steps):
+        for (i, e0, e1), grad, word, step in zip(self.slices, self.grads, self.words, self.steps):
             dys, xs, offsets = factors[i]
-            muon_expert_weight_grad(dys, xs, offsets[e0:e1 + 1], out=grad)
+            muon_expert_weight_grad(dys, xs, offsets[e0:e1 + 1], out=grad, status=word)
             step(stream=handle)
 
     @property
     def status(self) -> torch.Tensor:
-        """The blocks' status words, in the order of the stacks, their experts and blocks."""
-        return torch.cat([s.status_in_param_order() for s in self.steps])
+        """The blocks' status words, each with its slice's weight gradients' word, in the order of the stacks,
+        their experts and blocks."""
+        return torch.cat([s.status_in_param_order() | word for s, word in zip(self.steps, self.words)])

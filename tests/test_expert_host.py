@@ -236,3 +236,18 @@ def test_products_of_too_many_weight_rows(lib):
     assert lib.muon_expert_product(P, 8, P, 8, 8 * outer, P, 512, 10, 8, outer, 0, P, outer, None, 0, None, None) == -1
     assert lib.muon_expert_input_grad(P, outer, P, 8, 8 * outer, P, 512, 10, 8, outer, 0, P, 8, None, 0, None, None) == -1
     assert lib.muon_expert_weight_grad(P, outer, P, 8, P, 512, 10, 8, outer, 0, P, 8, 8 * outer, 0, 0, None, 0, None, None) == -1
+
+
+def test_a_timed_out_weight_gradient_flags_its_slice():
+    """ExpertMuonStep.status: the word of a slice's weight gradients reaches every block of that slice, and no other."""
+    class Step:
+        def __init__(self, words):
+            self.words = torch.tensor(words, dtype=torch.int32)
+
+        def status_in_param_order(self):
+            return self.words
+
+    step = nsm.ExpertMuonStep.__new__(nsm.ExpertMuonStep)
+    step.steps = [Step([0, 1, 0]), Step([0, 0]), Step([1])]
+    step.words = torch.tensor([2, 0, 2], dtype=torch.int32).split(1)
+    assert step.status.tolist() == [2, 3, 2, 0, 0, 3]

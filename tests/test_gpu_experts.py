@@ -638,3 +638,22 @@ def test_products_of_permuted_stacks(counts, inner, outer, dtype):
         nsm.muon_expert_weight_grad(dys, xs, offsets, out=dense, accumulate=accumulate)
         assert torch.equal(out, dense)
         assert bool((store[outer:] == 7).all()) and bool((store[:, len(counts):] == 7).all())
+
+
+def test_expert_step_reports_its_weight_gradients():
+    """Every slice has a word that its weight gradients write, eagerly and replayed; a set one flags the slice's blocks."""
+    g = gen(43)
+    w, m = randn(g, 3, 64, 32, dtype=BF), torch.zeros(3, 64, 32, device="cuda")
+    step = nsm.ExpertMuonStep([w], [m], blocks=[(32, 32)], slice_bytes=1)
+    factors = [(randn(g, 12, 64, dtype=BF), randn(g, 12, 32, dtype=BF), offsets_of([3, 5, 4]))]
+    step(factors)
+    assert len(step.words) == 3 and step.status.tolist() == [0] * 6
+    step.words[1].fill_(2)
+    assert step.status.tolist() == [0, 0, 2, 2, 0, 0]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(factors)
+    for run in (graph.replay, lambda: step(factors)):
+        step.words[1].fill_(2)
+        run()
+        assert step.status.tolist() == [0] * 6
