@@ -268,6 +268,23 @@ def _pitch(t: torch.Tensor, name: str) -> int:
     return ld
 
 
+def _apart(t: torch.Tensor, name: str):
+    """Refuses a tensor to be written whose rows share memory: a leading stride of zero, windows that overlap."""
+    cols, lead = t.shape[-1], sorted((s, n) for s, n in zip(t.stride()[:-1], t.shape[:-1]) if n > 1)
+    span = cols  # elements from the first to the last of the dimensions so far
+    for stride, n in lead:
+        if stride < span:
+            break
+        span += (n - 1) * stride
+    else:
+        return
+    starts = torch.zeros(1, dtype=torch.int64)  # strides that interleave: the rows themselves
+    for stride, n in lead:
+        starts = (starts[:, None] + stride * torch.arange(n)).view(-1)
+    if bool((starts.sort().values.diff() < cols).any()):
+        raise MuonError(f"{name} overlaps itself")
+
+
 def _build_block_groups(params, grads, moms, blocks):
     """Block groups in first-appearance order, and the index of every grouped
     block in the order of the parameters' blocks (matrices, block rows, block
@@ -287,6 +304,8 @@ def _build_block_groups(params, grads, moms, blocks):
             raise MuonError("param, grad and momentum shapes differ")
         if m.dtype != torch.float32:
             raise MuonError("momentum buffers must be float32")
+        _apart(w, "param")
+        _apart(m, "momentum")
         rows, cols = w.shape[-2:]
         r, c = (rows, cols) if block is None else (int(block[0]), int(block[1]))
         if r < 1 or c < 1 or rows % r or cols % c:
@@ -411,8 +430,9 @@ def muon_step_blocks(params: Sequence[torch.Tensor], grads: Sequence[torch.Tenso
     place on ``params`` and ``moms``.
 
     A parameter is (..., R, C) with contiguous rows and any other strides (an
-    expert stack, a fused gate and up, a slice of either); its entry in
-    ``blocks`` is the (rows, cols) of the blocks that tile each of its
+    expert stack, a fused gate and up, a slice of either; a gradient's matrices
+    may be the same memory, those of parameters and momentum buffers must not
+    overlap, in one tensor or between them); its entry in ``blocks`` is the (rows, cols) of the blocks that tile each of its
     matrices, or None for whole matrices.  Every block is orthogonalised on its
     own, as muon_step does a matrix: (head_dim, hidden) splits a query
     projection into heads, (hidden, head_dim) an output projection.  ``status``
@@ -965,6 +985,7 @@ def muon_expert_weight_grad(dys: torch.Tensor, xs: torch.Tensor, offsets: torch.
         if out.shape != (experts, outer, inner):
             raise MuonError(f"out must be {(experts, outer, inner)}, not {tuple(out.shape)}")
         _, _, ld_out, stride_out = _stack_arg(out, "out", experts, device, out.dtype)
+        _apart(out, "out")
     if not _here(device, stream):
         return _elsewhere(device, stream, muon_expert_weight_grad, dys, xs, offsets, out=out, out_dtype=out_dtype,
                           accumulate=accumulate, status=status)
@@ -1009,6 +1030,11 @@ class ExpertMuonStep:
         for w in params:
             if not w.is_cuda or w.dim() != 3 or w.device != params[0].device:
                 raise MuonError("params must be (experts, outer, inner) stacks on one device")
+        for w, m in zip(params, moms):  # the slices are checked one by one below
+            if w.shape != m.shape:
+                raise MuonError("param and momentum shapes differ")
+            _apart(w, "param")
+            _apart(m, "momentum")
         self.device = params[0].device
         self.shapes = [tuple(w.shape) for w in params]
         dtypes = self.dtypes = [grad_dtype or w.dtype for w in params]

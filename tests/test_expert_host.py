@@ -251,3 +251,23 @@ def test_a_timed_out_weight_gradient_flags_its_slice():
     step.steps = [Step([0, 1, 0]), Step([0, 0]), Step([1])]
     step.words = torch.tensor([2, 0, 2], dtype=torch.int32).split(1)
     assert step.status.tolist() == [2, 3, 2, 0, 0, 3]
+
+
+def test_blocks_that_share_memory_are_refused():
+    """Two blocks of one launch must not update the same memory; gradients may be broadcast."""
+    sf = torch.float32
+    good, mom = Fake((2, 4, 6)), Fake((2, 4, 6), dtype=sf)
+    for strides in ((0, 6, 1), (12, 6, 1), (23, 6, 1), (5, 10, 1), (6, 6, 1)):
+        for call in (lambda t, m: nsm._build_block_groups([t], [good], [m], [(2, 3)]),
+                     lambda t, m: nsm.ExpertMuonStep([t], [m], slice_bytes=1)):
+            with pytest.raises(nsm.MuonError, match="overlaps"):
+                call(Fake((2, 4, 6), strides), mom)
+            with pytest.raises(nsm.MuonError, match="overlaps"):
+                call(good, Fake((2, 4, 6), strides, dtype=sf))
+        with pytest.raises(nsm.MuonError, match="overlaps"):
+            nsm.muon_expert_weight_grad(Fake((5, 4)), Fake((5, 6)), Fake((3,), dtype=torch.int32), out=Fake((2, 4, 6), strides))
+        assert nsm._build_block_groups([good], [Fake((2, 4, 6), (strides[0], 6, 1))], [mom], [None])[1] == 1
+    # the experts of a permuted stack, the halves of fused columns, rows that interleave without meeting
+    for strides in ((6, 12, 1), (6, 20, 1), (24, 6, 1), (9, 18, 1), (7, 15, 1)):
+        assert nsm._build_block_groups([Fake((2, 4, 6), strides)], [good], [Fake((2, 4, 6), strides, dtype=sf)], [None])[1] == 1
+    assert nsm._build_block_groups([Fake((3, 2, 2), (4, 6, 1))], [Fake((3, 2, 2))], [Fake((3, 2, 2), dtype=sf)], [None])[1] == 1
