@@ -1028,8 +1028,8 @@ class ExpertMuonStep:
         if len(blocks) != len(params):
             raise MuonError("blocks must have one entry per parameter")
         for w in params:
-            if not w.is_cuda or w.dim() != 3 or w.device != params[0].device:
-                raise MuonError("params must be (experts, outer, inner) stacks on one device")
+            if not w.is_cuda or w.dim() != 3 or w.device != params[0].device or w.numel() == 0:
+                raise MuonError("params must be (experts, outer, inner) stacks on one device, none of them empty")
         for w, m in zip(params, moms):  # the slices are checked one by one below
             if w.shape != m.shape:
                 raise MuonError("param and momentum shapes differ")

@@ -271,3 +271,9 @@ def test_blocks_that_share_memory_are_refused():
     for strides in ((6, 12, 1), (6, 20, 1), (24, 6, 1), (9, 18, 1), (7, 15, 1)):
         assert nsm._build_block_groups([Fake((2, 4, 6), strides)], [good], [Fake((2, 4, 6), strides, dtype=sf)], [None])[1] == 1
     assert nsm._build_block_groups([Fake((3, 2, 2), (4, 6, 1))], [Fake((3, 2, 2))], [Fake((3, 2, 2), dtype=sf)], [None])[1] == 1
+
+
+@pytest.mark.parametrize("shape", [(0, 4, 8), (2, 0, 8), (2, 4, 0)])
+def test_empty_stacks_are_refused(shape):
+    with pytest.raises(nsm.MuonError):
+        nsm.ExpertMuonStep([Fake(shape)], [Fake(shape, dtype=torch.float32)])
