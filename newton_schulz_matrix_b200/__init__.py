@@ -46,6 +46,7 @@ EXPORTED_SYMBOLS = (
     "muon_expert_workspace_size",
 )
 EXPERT_MAX = 1024
+_EXPERT_MOST = 1 << 30  # rows, columns and tokens * topk of the expert operators
 NOALLOC_SCRATCH_BYTES = 64 << 20
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -218,6 +219,12 @@ def _raise(rc: int, what: str):
         raise MuonError(f"{what} failed: {rc} ({muon_status_string(rc)})")
 
 
+def _sides(*sizes):
+    """Refuses matrix sizes that the C structs' ints cannot hold (ctypes would keep their low 32 bits)."""
+    if max(sizes) >= 1 << 31:
+        raise MuonError(f"matrices have fewer than 2^31 rows and columns, not {max(sizes)}")
+
+
 def _build_groups(params, grads, moms):
     """Group tensors by (shape, W dtype, G dtype) in first-appearance order."""
     keys = []
@@ -228,6 +235,7 @@ def _build_groups(params, grads, moms):
             raise MuonError("param, grad and momentum shapes differ")
         if m.dtype != torch.float32:
             raise MuonError("momentum buffers must be float32")
+        _sides(*w.shape)
         k = (tuple(w.shape), _dtype_code(w.dtype), _dtype_code(g.dtype))
         if k not in index:
             index[k] = len(keys)
@@ -307,6 +315,7 @@ def _build_block_groups(params, grads, moms, blocks):
         _apart(w, "param")
         _apart(m, "momentum")
         rows, cols = w.shape[-2:]
+        _sides(rows, cols)
         r, c = (rows, cols) if block is None else (int(block[0]), int(block[1]))
         if r < 1 or c < 1 or rows % r or cols % c:
             raise MuonError(f"blocks of {r} x {c} do not tile a {rows} x {cols} matrix")
@@ -492,6 +501,7 @@ def muon_ns_batched(X: Sequence[torch.Tensor], *, coeffs=(QUINTIC,) * 5, mode="s
         if t.shape != X[0].shape or t.dtype != X[0].dtype:
             raise MuonError("all matrices must share shape and dtype")
     rows, cols = X[0].shape
+    _sides(rows, cols)
     dt = _dtype_code(X[0].dtype)
     if compute_dtype is None:
         compute_dtype = "fp32" if dt == FP32 else "fp16"
@@ -606,6 +616,7 @@ def muon_ns_batched_noalloc(X: Sequence[torch.Tensor], *, coeffs=(QUINTIC,) * 5,
         if t.shape != X[0].shape or t.dtype != X[0].dtype:
             raise MuonError("all matrices must share shape and dtype")
     rows, cols = X[0].shape
+    _sides(rows, cols)
     dt = _dtype_code(X[0].dtype)
     if compute_dtype is None:
         compute_dtype = "fp32" if dt == FP32 else "fp16"
@@ -738,6 +749,8 @@ def _lead(t: torch.Tensor, name: str):
     dtype, (rows, cols) = t.dtype, t.shape
     if dtype not in _CODES:
         raise MuonError(f"unsupported dtype {dtype}")
+    if rows > _EXPERT_MOST or cols > _EXPERT_MOST:
+        raise MuonError(f"{name} has more than 2^30 rows or columns: {rows} x {cols}")
     return t.device, dtype, _CODES[dtype], rows, cols, _pitch(t, name)
 
 
@@ -747,6 +760,8 @@ def _slot_arg(slot: torch.Tensor, device: torch.device):
     tokens, topk = slot.shape
     if topk < 1:
         raise MuonError("slot must have at least one column")
+    if tokens * topk > _EXPERT_MOST:
+        raise MuonError(f"slot has more than 2^30 entries: {tokens} x {topk}")
     return tokens, topk
 
 
@@ -772,7 +787,9 @@ def muon_expert_sort(ids: torch.Tensor, experts: int, *, workspace: torch.Tensor
     device = ids.device
     lib = load_library()
     tokens, topk = ids.shape
-    need = lib.muon_expert_sort_workspace_size(tokens, topk, experts)
+    need = 0
+    if tokens * topk <= _EXPERT_MOST and topk <= _EXPERT_MOST and 0 < experts <= EXPERT_MAX:
+        need = lib.muon_expert_sort_workspace_size(tokens, topk, experts)
     if need == 0:
         raise MuonError(f"cannot sort {tokens} x {topk} assignments to {experts} experts (workspace query returned 0)")
     ld, n, es = _pitch(ids, "ids"), tokens * topk, ids.element_size()
@@ -871,8 +888,9 @@ def muon_expert_combine_backward(dy: torch.Tensor, ys: torch.Tensor, slot: torch
 
 def _offsets_arg(offsets: torch.Tensor, device: torch.device) -> int:
     if offsets.device != device or offsets.dtype != torch.int32 or offsets.dim() != 1 or \
-            not offsets.is_contiguous() or offsets.shape[0] < 2:
-        raise MuonError("offsets must be a contiguous int32 tensor of experts + 1 entries on the rows' device")
+            not offsets.is_contiguous() or not 2 <= offsets.shape[0] <= EXPERT_MAX + 1:
+        raise MuonError(f"offsets must be a contiguous int32 tensor of experts + 1 entries on the rows' device, for at "
+                        f"most {EXPERT_MAX} experts")
     return offsets.shape[0] - 1
 
 
@@ -882,6 +900,8 @@ def _stack_arg(w: torch.Tensor, name: str, experts: int, device: torch.device, d
         raise MuonError(f"{name} must be {dtype} ({experts}, outer, inner) on {device}, not {w.dtype} {tuple(w.shape)} "
                         f"on {w.device}")
     _, outer, inner = w.shape
+    if outer > _EXPERT_MOST or inner > _EXPERT_MOST:
+        raise MuonError(f"{name} has more than 2^30 rows or columns an expert: {outer} x {inner}")
     return outer, inner, _pitch(w, name), w.stride(0) if experts > 1 else outer * inner
 
 
@@ -968,7 +988,9 @@ def muon_expert_weight_grad(dys: torch.Tensor, xs: torch.Tensor, offsets: torch.
     ``accumulate`` adds to a float32 ``out`` (gradient accumulation).
     """
     device, dtype, code, rows, outer, ld_dys = _lead(dys, "dys")
-    inner = xs.shape[-1]
+    if xs.dim() != 2 or xs.shape[1] > _EXPERT_MOST:
+        raise MuonError(f"xs must be a matrix of at most 2^30 columns, not {tuple(xs.shape)}")
+    inner = xs.shape[1]
     ld_xs = _matrix(xs, "xs", device, dtype, rows, inner)
     experts = _offsets_arg(offsets, device)
     word = _status_arg(status, device)

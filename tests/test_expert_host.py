@@ -277,3 +277,37 @@ def test_blocks_that_share_memory_are_refused():
 def test_empty_stacks_are_refused(shape):
     with pytest.raises(nsm.MuonError):
         nsm.ExpertMuonStep([Fake(shape)], [Fake(shape, dtype=torch.float32)])
+
+
+def test_sizes_that_pass_32_bits_are_refused():
+    """ctypes keeps the low 32 bits of an int argument: 2^32 + 4 tokens must not be sorted as 4."""
+    i32, sf, big = torch.int32, torch.float32, 2 ** 32
+    offsets, few, tall, wide = Fake((2,), dtype=i32), Fake((4, 8)), Fake((big + 4, 8)), Fake((1, big + 8))
+    calls = [
+        lambda: nsm.muon_expert_sort(Fake((big + 4, 1), dtype=i32), 8),
+        lambda: nsm.muon_expert_sort(Fake((0, big + 1), dtype=i32), 8),
+        lambda: nsm.muon_expert_sort(Fake((4, 2), dtype=i32), big + 8),
+        lambda: nsm.muon_expert_gather(tall, Fake((big + 4, 1), dtype=i32)),
+        lambda: nsm.muon_expert_gather(wide, Fake((1, 1), dtype=i32)),
+        lambda: nsm.muon_expert_combine(few, Fake((big + 4, 1), dtype=i32)),
+        lambda: nsm.muon_expert_combine(few, Fake((1 << 29, 4), dtype=i32)),
+        lambda: nsm.muon_expert_combine(wide, Fake((1, 1), dtype=i32)),
+        lambda: nsm.muon_expert_combine_backward(Fake((big + 4, 8)), few, Fake((big + 4, 1), dtype=i32)),
+        lambda: nsm.muon_expert_product(few, Fake((1, big + 8, 8)), offsets),
+        lambda: nsm.muon_expert_product(wide, Fake((1, 1, big + 8)), offsets),
+        lambda: nsm.muon_expert_input_grad(wide, Fake((1, big + 8, 1)), offsets),
+        lambda: nsm.muon_expert_weight_grad(few, Fake((4, big + 8)), offsets),
+        lambda: nsm.muon_expert_weight_grad(few, few, Fake((big + 2,), dtype=i32)),
+    ]
+    for t, m in ((wide, Fake((1, big + 8), dtype=sf)), (Fake((big + 8, 1)), Fake((big + 8, 1), dtype=sf))):
+        calls += [lambda t=t, m=m: nsm.muon_step_blocks([t], [t], [m], [None]),
+                  lambda t=t, m=m: nsm.muon_blocks_workspace_size([t], [t], [m], [(1, 1)]),
+                  lambda t=t, m=m: nsm.muon_step([t], [t], [m]),
+                  lambda t=t: nsm.muon_ns_batched([t]), lambda t=t: nsm.muon_ns_batched_noalloc([t])]
+    for i, call in enumerate(calls):
+        try:
+            call()
+        except nsm.MuonError as e:
+            assert "CUDA" not in str(e), (i, e)  # refused for its size, not by a launch
+        else:
+            raise AssertionError(i)
