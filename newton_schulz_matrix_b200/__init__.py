@@ -468,7 +468,10 @@ def muon_step_blocks(params: Sequence[torch.Tensor], grads: Sequence[torch.Tenso
                                 None if grouped is None else grouped.data_ptr(), _raw_stream(device.index)),
            "muon_step_blocks")
     if status is not None:
-        status.view(-1)[torch.tensor(order, device=device)] = grouped
+        # words in a row at a time: an index tensor would have to come from the host, which a capture forbids
+        flat, at = status.view(-1), [k for k, o in enumerate(order) if k == 0 or o != order[k - 1] + 1] + [len(order)]
+        torch._foreach_copy_([flat[order[a]:order[a] + b - a] for a, b in zip(at, at[1:])],
+                             [grouped[a:b] for a, b in zip(at, at[1:])])
     return status
 
 

@@ -286,3 +286,23 @@ def test_small_blocks_that_one_launch_does_not_take(block, hp):
     assert status.tolist() == [0] * 4
     for got, want in zip(cut(w, block) + cut(m, block), wd + md):
         assert torch.equal(got, want)
+
+
+def test_a_block_step_with_status_words_can_be_captured():
+    """Kinds of blocks that take turns, so that the words come back in another order than the groups'."""
+    shapes = [((4, 64, 96), (32, 96)), ((128, 80), (64, 40)), ((2, 64, 96), (32, 96)), ((64, 40), None), ((3, 64, 96), (32, 96))]
+    (ws, gs, ms) = ([make(s, None, dt, 180 + 3 * i + k, std)[0] for i, (s, _) in enumerate(shapes)]
+                    for k, (dt, std) in enumerate(((torch.bfloat16, 0.05), (torch.bfloat16, 1.0), (torch.float32, 0.2))))
+    blocks = [b for _, b in shapes]
+    gs[1][64:, 40:] = float("nan")  # the last of the second parameter's four blocks
+    gs[4][1, :32, :32] = float("nan")  # the third of the last one's six
+    want = [0] * 8 + [0, 0, 0, 1] + [0] * 4 + [0] + [0, 0, 1, 0, 0, 0]
+    status = torch.full((len(want),), -1, dtype=torch.int32, device="cuda")
+    assert nsm.muon_step_blocks(ws, gs, ms, blocks, status=status) is status
+    assert status.tolist() == want
+    shaped = torch.full((1, len(want)), -1, dtype=torch.int32, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        nsm.muon_step_blocks(ws, gs, ms, blocks, status=shaped)
+    graph.replay()
+    assert shaped[0].tolist()[8:12] == want[8:12] and shaped[0].tolist()[17:] == want[17:]
