@@ -205,6 +205,13 @@ def _here(device: torch.device, stream) -> bool:
     return stream is None and device.index == torch.cuda.current_device()
 
 
+def _check_workspace(ws: torch.Tensor, device: torch.device):
+    if ws.device != device:
+        raise MuonError(f"the workspace is on {ws.device}, the tensors on {device}")
+    if not ws.is_contiguous():
+        raise MuonError("the workspace must be contiguous")
+
+
 def _check_cuda(t: torch.Tensor, name: str):
     if not t.is_cuda:
         raise MuonError(f"{name} must be a CUDA tensor")
@@ -454,11 +461,11 @@ def muon_step_blocks(params: Sequence[torch.Tensor], grads: Sequence[torch.Tenso
     if need == 0:
         raise MuonError("invalid arguments (workspace query returned 0)")
     device = params[0].device
-    if status is not None and (status.dtype != torch.int32 or status.numel() != len(order) or status.device != device):
-        raise MuonError(f"status must be an int32 tensor of {len(order)} words on the parameters' device")
-
-    if workspace is not None and workspace.device != device:
-        raise MuonError(f"the workspace is on {workspace.device}, the parameters on {device}")
+    if status is not None and (status.dtype != torch.int32 or status.numel() != len(order) or
+                               status.device != device or not status.is_contiguous()):
+        raise MuonError(f"status must be a contiguous int32 tensor of {len(order)} words on the parameters' device")
+    if workspace is not None:
+        _check_workspace(workspace, device)
     if not _here(device, stream):
         return _elsewhere(device, stream, muon_step_blocks, params, grads, moms, blocks, workspace=workspace,
                           status=status, **hp)
@@ -563,6 +570,7 @@ class MuonStep:
             raise MuonError("invalid arguments (workspace query returned 0)")
         self.workspace_needed = (lo, full)
         if workspace is not None:
+            _check_workspace(workspace, params[0].device)
             if workspace.numel() * workspace.element_size() < lo:
                 raise MuonError(f"workspace of {workspace.numel()} bytes is below the minimum {lo}")
             self.workspace = workspace
@@ -576,7 +584,7 @@ class MuonStep:
         if not _here(self.workspace.device, None):  # the tensors' device, not the current one
             return _elsewhere(self.workspace.device, stream, self)
         rc = self._step(self._groups, self._ng, ctypes.byref(self._h), ctypes.c_void_p(self.workspace.data_ptr()),
-                        ctypes.c_size_t(self.workspace.numel()), ctypes.c_void_p(self.status.data_ptr()),
+                        ctypes.c_size_t(self.workspace.nbytes), ctypes.c_void_p(self.status.data_ptr()),
                         ctypes.c_void_p(_stream_handle(stream)))
         _raise(rc, self._name)
 
@@ -796,13 +804,13 @@ def muon_expert_sort(ids: torch.Tensor, experts: int, *, workspace: torch.Tensor
     if need == 0:
         raise MuonError(f"cannot sort {tokens} x {topk} assignments to {experts} experts (workspace query returned 0)")
     ld, n, es = _pitch(ids, "ids"), tokens * topk, ids.element_size()
+    if workspace is not None:
+        _check_workspace(workspace, device)
     if not _here(device, stream):
         return _elsewhere(device, stream, muon_expert_sort, ids, experts, workspace=workspace)
     out = torch.empty(experts + 1 + 2 * n, dtype=torch.int32, device=device)
     offsets, slot, source = out.split_with_sizes((experts + 1, n, n))
     ws, ws_bytes = workspace, 0
-    if ws is not None and ws.device != device:
-        raise MuonError(f"the workspace is on {ws.device}, ids on {device}")
     if ws is None and need > 256:
         ws = torch.empty(need, dtype=torch.uint8, device=device)
     if ws is not None:

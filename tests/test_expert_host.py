@@ -311,3 +311,18 @@ def test_sizes_that_pass_32_bits_are_refused():
             assert "CUDA" not in str(e), (i, e)  # refused for its size, not by a launch
         else:
             raise AssertionError(i)
+
+
+def test_status_and_workspace_are_checked_before_the_step():
+    """A strided status would be refused by the copy behind the step, a strided workspace would be written in its gaps."""
+    w, m, i32, u8 = Fake((2, 4, 8)), Fake((2, 4, 8), dtype=torch.float32), torch.int32, torch.uint8
+    step = lambda **kw: nsm.muon_step_blocks([w], [w], [m], [None], **kw)
+    ids = Fake((1 << 17, 8), dtype=i32)
+    for call in (lambda: step(status=Fake((2,), (2,), dtype=i32)), lambda: step(workspace=Fake((1 << 24,), (2,), dtype=u8)),
+                 lambda: step(workspace=Fake((1 << 24,), dtype=u8, device="cuda:1")),
+                 lambda: nsm.muon_expert_sort(ids, 8, workspace=Fake((1 << 24,), (2,), dtype=u8)),
+                 lambda: nsm.muon_expert_sort(ids, 8, workspace=Fake((1 << 24,), dtype=u8, device="cuda:1")),
+                 lambda: nsm.MuonStep([w], [w], [m], blocks=[None], workspace=Fake((1 << 24,), (2,), dtype=u8)),
+                 lambda: nsm.MuonStep([w], [w], [m], blocks=[None], workspace=Fake((1 << 24,), dtype=u8, device="cuda:1"))):
+        with pytest.raises(nsm.MuonError, match="contiguous|is on"):
+            call()

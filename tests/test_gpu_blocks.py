@@ -306,3 +306,12 @@ def test_a_block_step_with_status_words_can_be_captured():
         nsm.muon_step_blocks(ws, gs, ms, blocks, status=shaped)
     graph.replay()
     assert shaped[0].tolist()[8:12] == want[8:12] and shaped[0].tolist()[17:] == want[17:]
+
+
+def test_a_workspace_of_another_type_counts_its_bytes():
+    w, g, m = (make((2, 256, 320), None, dt, 200 + i, s)[0] for i, (dt, s) in enumerate(
+        ((torch.bfloat16, 0.05), (torch.bfloat16, 1.0), (torch.float32, 0.2))))
+    lo = nsm.muon_blocks_workspace_min([w], [g], [m], [None])
+    step = nsm.MuonStep([w], [g], [m], blocks=[None], workspace=torch.empty(-(-lo // 4), dtype=torch.float32, device="cuda"))
+    step()
+    assert step.status.tolist() == [0, 0]
