@@ -168,7 +168,9 @@ typedef struct {
  * The results are muon_step's on dense copies of the blocks, bit for bit, except
  * for blocks with min(rows, cols) <= 128 and max <= 4096 in 16-bit standard chains
  * of at most 64 iterations: they run in one launch, which adds up X X^T in another
- * order, and differ by the chain's roundings. */
+ * order, and differ by the chain's roundings.  That launch takes up to 512 blocks
+ * whatever the workspace holds: the sizes count such blocks like others, and
+ * muon_blocks_workspace_min is enough for its full speed. */
 MUON_API size_t muon_blocks_workspace_size(const muon_block_group* groups, int n_groups, const muon_hparams* hp);
 MUON_API size_t muon_blocks_workspace_min(const muon_block_group* groups, int n_groups, const muon_hparams* hp);
 MUON_API int muon_step_blocks(const muon_block_group* groups, int n_groups, const muon_hparams* hp, void* ws,

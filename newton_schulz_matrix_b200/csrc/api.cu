@@ -642,14 +642,15 @@ int run_batches(const std::vector<Batch>& batches, const std::vector<GroupView>&
     const bool fuse = one_launch || (update && rows_ok && ns->compute_dtype != MUON_FP32 && fused_update_enabled() &&
                                      gemm_tc_paired(L.n));
     int chunk_cap = (int)std::min<size_t>((size_t)bt.total, (ws_bytes - L.fixed) / L.per_matrix);
+    if (one_launch) chunk_cap = bt.total;  // it needs the error word of the workspace and nothing per block
     if (fuse) chunk_cap = std::min(chunk_cap, UpdateSlots::kMax);
     // slots are assigned in segment order; walk them chunk by chunk
     int seg_i = 0, seg_off = 0;
     int done = 0;
     while (done < bt.total) {
       const int chunk = std::min(chunk_cap, bt.total - done);
-      const Bufs B = carve(L, chunk, ws);
-      if (cudaMemsetAsync(B.err, 0, B.zero_bytes, s) != cudaSuccess) return MUON_ERR_CUDA;
+      const Bufs B = carve(L, one_launch ? 1 : chunk, ws);
+      if (cudaMemsetAsync(B.err, 0, one_launch ? sizeof(int) : B.zero_bytes, s) != cudaSuccess) return MUON_ERR_CUDA;
       // pieces of segments covering slots [done, done + chunk)
       struct Piece { int group, first, count, slot; };
       std::vector<Piece> pieces;

@@ -315,3 +315,19 @@ def test_a_workspace_of_another_type_counts_its_bytes():
     step = nsm.MuonStep([w], [g], [m], blocks=[None], workspace=torch.empty(-(-lo // 4), dtype=torch.float32, device="cuda"))
     step()
     assert step.status.tolist() == [0, 0]
+
+
+def test_one_launch_does_not_shrink_with_the_workspace():
+    """The least workspace takes as many blocks a launch as the largest one, and writes nothing behind its end."""
+    (w, _), (g, _), (m, _) = (make((600, 8, 256), None, dt, 210 + i, s) for i, (dt, s) in enumerate(
+        ((torch.bfloat16, 0.05), (torch.bfloat16, 1.0), (torch.float32, 0.2))))
+    w2, m2 = w.clone(), m.clone()
+    lo = nsm.muon_blocks_workspace_min([w], [g], [m], [None])
+    store = torch.full((lo + 4096,), 7, dtype=torch.uint8, device="cuda")
+    launches = []
+    for (a, b), ws in (((w, m), None), ((w2, m2), store[:lo])):
+        nsm.muon_profile_begin()
+        nsm.muon_step_blocks([a], [g], [b], [None], workspace=ws)
+        launches.append({r["kernel"]: r["launches"] for r in nsm.muon_profile_end()}["ns_block_kernel"])
+    assert launches == [2, 2]
+    assert torch.equal(w, w2) and torch.equal(m, m2) and bool((store[lo:] == 7).all())
