@@ -943,23 +943,35 @@ double flops_of(int rows, int cols, const muon_ns_params* ns) {
 extern "C" {
 
 size_t muon_workspace_size(const muon_group* groups, int n_groups, const muon_hparams* hp) {
-  std::vector<GroupView> views;
-  if (check_groups(groups, n_groups, hp, &views) != MUON_OK) return 0;
-  return ws_for(plan_groups(views), &hp->ns, true);
+  try {
+    std::vector<GroupView> views;
+    if (check_groups(groups, n_groups, hp, &views) != MUON_OK) return 0;
+    return ws_for(plan_groups(views), &hp->ns, true);
+  } catch (...) {  // std::bad_alloc: no exception crosses the C ABI
+    return 0;
+  }
 }
 
 size_t muon_workspace_min(const muon_group* groups, int n_groups, const muon_hparams* hp) {
-  std::vector<GroupView> views;
-  if (check_groups(groups, n_groups, hp, &views) != MUON_OK) return 0;
-  return ws_for(plan_groups(views), &hp->ns, false);
+  try {
+    std::vector<GroupView> views;
+    if (check_groups(groups, n_groups, hp, &views) != MUON_OK) return 0;
+    return ws_for(plan_groups(views), &hp->ns, false);
+  } catch (...) {  // std::bad_alloc: no exception crosses the C ABI
+    return 0;
+  }
 }
 
 int muon_step(const muon_group* groups, int n_groups, const muon_hparams* hp, void* ws, size_t ws_bytes,
               int* status_per_matrix, void* stream) {
-  std::vector<GroupView> views;
-  const int rc = check_groups(groups, n_groups, hp, &views);
-  if (rc != MUON_OK) return rc;
-  return step_views(views, false, hp, ws, ws_bytes, status_per_matrix, reinterpret_cast<cudaStream_t>(stream));
+  try {
+    std::vector<GroupView> views;
+    const int rc = check_groups(groups, n_groups, hp, &views);
+    if (rc != MUON_OK) return rc;
+    return step_views(views, false, hp, ws, ws_bytes, status_per_matrix, reinterpret_cast<cudaStream_t>(stream));
+  } catch (...) {  // std::bad_alloc: no exception crosses the C ABI
+    return MUON_ERR_INVALID;
+  }
 }
 
 size_t muon_blocks_workspace_size(const muon_block_group* groups, int n_groups, const muon_hparams* hp) {
@@ -1010,15 +1022,19 @@ int muon_ns_batched(void* const* X, int count, int rows, int cols, int dtype, co
     if (!X[i] || !aligned16(X[i])) return MUON_ERR_INVALID;
   if (!ws || (reinterpret_cast<uintptr_t>(ws) & (kAlign - 1))) return MUON_ERR_INVALID;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  Batch b{std::min(rows, cols), std::max(rows, cols), {Seg{0, 0, count}}, count};
-  std::vector<Batch> batches{b};
-  if (ws_bytes < ws_for(batches, ns, false)) return MUON_ERR_WORKSPACE;
-  std::vector<GroupView> views{GroupView{rows, cols, count, dtype, dtype, cols, cols, cols,
-                                         const_cast<const void* const*>(X), nullptr, X}};
-  std::vector<long long> first{0};
-  if (status_per_matrix && cudaMemsetAsync(status_per_matrix, 0, (size_t)count * sizeof(int), s) != cudaSuccess)
-    return MUON_ERR_CUDA;
-  return run_batches(batches, views, first, ns, false, false, 0.f, 0, 0.f, 0.f, 0.f, ws, ws_bytes, status_per_matrix, s);
+  try {
+    Batch b{std::min(rows, cols), std::max(rows, cols), {Seg{0, 0, count}}, count};
+    std::vector<Batch> batches{b};
+    if (ws_bytes < ws_for(batches, ns, false)) return MUON_ERR_WORKSPACE;
+    std::vector<GroupView> views{GroupView{rows, cols, count, dtype, dtype, cols, cols, cols,
+                                           const_cast<const void* const*>(X), nullptr, X}};
+    std::vector<long long> first{0};
+    if (status_per_matrix && cudaMemsetAsync(status_per_matrix, 0, (size_t)count * sizeof(int), s) != cudaSuccess)
+      return MUON_ERR_CUDA;
+    return run_batches(batches, views, first, ns, false, false, 0.f, 0, 0.f, 0.f, 0.f, ws, ws_bytes, status_per_matrix, s);
+  } catch (...) {  // std::bad_alloc: no exception crosses the C ABI
+    return MUON_ERR_INVALID;
+  }
 }
 
 double muon_ns_flops(int rows, int cols, const muon_ns_params* ns) {

@@ -44,8 +44,13 @@ struct ProfScope {
     if (!active) return;
     cudaEventRecord(rec.b, s);
     Profiler& P = profiler();
-    std::lock_guard<std::mutex> g(P.mu);
-    P.recs.push_back(rec);
+    try {
+      std::lock_guard<std::mutex> g(P.mu);
+      P.recs.push_back(rec);
+    } catch (...) {  // std::bad_alloc: the launch has gone out, it is not profiled
+      cudaEventDestroy(rec.a);
+      cudaEventDestroy(rec.b);
+    }
   }
 };
 

@@ -1,12 +1,16 @@
 """Host-only checks of the expert-layer operators and the block step: argument
 checks of the C ABI and of the binding, workspace sizes, without a GPU."""
 import ctypes
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
 
 import newton_schulz_matrix_b200 as nsm
 
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 P = 1 << 20  # a stand-in device pointer: nothing below launches
 
 
@@ -326,3 +330,33 @@ def test_status_and_workspace_are_checked_before_the_step():
                  lambda: nsm.MuonStep([w], [w], [m], blocks=[None], workspace=Fake((1 << 24,), dtype=u8, device="cuda:1"))):
         with pytest.raises(nsm.MuonError, match="contiguous|is on"):
             call()
+
+
+def test_no_exception_leaves_the_library(lib):
+    """Host memory that runs out is an error code, not std::terminate (in a process of its own, with a bounded address space)."""
+    code = """
+import ctypes, resource, sys
+sys.path.insert(0, {root!r})
+import newton_schulz_matrix_b200 as nsm
+lib = nsm.load_library()
+ns, keep = nsm._ns_params((nsm.QUINTIC,) * 5, "standard", 2, 1e-7, "fp16", "fp16")
+hp = nsm._hparams(0.02, 0.95, 0.1, 0.2, 1, ns)
+n = 1 << 22
+plain, blocks = (nsm._Group * n)(), (nsm._BlockGroup * n)()
+one, ld = nsm._Group(8, 8, 0, 0, 0), nsm._BlockGroup(8, 8, 0, 1, 1, 0, 0, 8, 8, 8)
+for array, item in ((plain, one), (blocks, ld)):
+    raw = bytes(item)
+    ctypes.memmove(array, raw * n, len(raw) * n)
+    del raw
+pages = int(open("/proc/self/statm").read().split()[0])
+limit = pages * resource.getpagesize() + (64 << 20)
+resource.setrlimit(resource.RLIMIT_AS, (limit, limit))
+ws = ctypes.c_void_p(1 << 24)
+for kind, array in (("muon", plain), ("muon_blocks", blocks)):
+    assert getattr(lib, kind + "_workspace_size")(array, n, ctypes.byref(hp)) == 0, kind
+    assert getattr(lib, kind + "_workspace_min")(array, n, ctypes.byref(hp)) == 0, kind
+assert lib.muon_step(plain, n, ctypes.byref(hp), ws, 1 << 30, None, None) == -1
+assert lib.muon_step_blocks(blocks, n, ctypes.byref(hp), ws, 1 << 30, None, None) == -1
+""".format(root=ROOT)
+    run = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert run.returncode == 0, (run.returncode, run.stderr[-500:])
