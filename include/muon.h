@@ -229,7 +229,8 @@ MUON_API int muon_ns_batched_noalloc(void* const* X, int count, int rows, int co
  * Sorted rows that no expert owns are neither read into a result nor written.  All sums are held
  * in fp32 and rounded once, in an order that does not change from call to call.
  * Rows, columns and tokens * topk are at most 2^30, experts at most 1024 and
- * experts * outer (all weights' rows) at most 2^34.
+ * experts * outer (all weights' rows) at most 2^34.  What a call writes overlaps
+ * nothing that it reads, unless its description says otherwise.
  *
  * muon_expert_sort: ids is tokens x topk of int32 or int64 (id_bytes 4 or 8),
  * row pitch ld_ids; an id outside [0, experts) goes to no expert.  The sort is
@@ -253,7 +254,7 @@ MUON_API int muon_expert_combine(const void* ys, long long ld_ys, long long rows
 /* The gradients of muon_expert_combine:
  *   dys[slot[t, j]]  = weights[t, j] * dy[t]
  *   dweights[t, j]   = <dy[t], ys[slot[t, j]]>, zero for an assignment that no expert takes
- * dweights (of w_dtype) may be NULL; ys is then not read. */
+ * dweights (of w_dtype) may be NULL; ys is then not read.  dys may be ys. */
 MUON_API int muon_expert_combine_backward(const void* dy, long long ld_dy, const void* ys, long long ld_ys, long long rows,
                                           const int* slot, const void* weights, int w_dtype, int tokens, int topk,
                                           int cols, int dtype, void* dys, long long ld_dys, void* dweights, void* stream);
@@ -261,7 +262,8 @@ MUON_API int muon_expert_combine_backward(const void* dy, long long ld_dy, const
 /* The experts' products.  W[e] is outer x inner at w + e * stride_w, row pitch
  * ld_w; xs is rows x inner, ys and dys are rows x outer, one dtype for all.
  * Offsets are clamped to [0, rows] and read on the device: no count reaches the
- * host.
+ * host.  They may run backwards; a row that several experts then own gets one
+ * expert's product, of no particular one.
  *   muon_expert_product       y[p]   = W[e] xs[p]            for e's rows p
  *   muon_expert_input_grad    dxs[p] = W[e]^T dys[p]         for e's rows p
  *   muon_expert_weight_grad   dW[e]  = sum_p dys[p] xs[p]^T  over e's rows p
@@ -272,12 +274,15 @@ MUON_API int muon_expert_combine_backward(const void* dy, long long ld_dy, const
  * such rows in the workspace, where it holds muon_expert_workspace_size bytes;
  * without it, where that is 0 (small products), and in fp32 the CUDA cores run.
  * status: one optional device word, zeroed by the call, MUON_STATUS_TIMEOUT when
- * a device-side wait gave up. */
+ * a device-side wait gave up and part of the result was not written.  Without a word
+ * nothing reports that, as with the status words of muon_step. */
 enum { MUON_EXPERT_PRODUCT = 0, MUON_EXPERT_INPUT_GRAD = 1, MUON_EXPERT_WEIGHT_GRAD = 2 };
 /* Workspace bytes with which the product `kind` of these operands runs on the
  * tensor cores (a: xs or dys, b: w, or xs for the weight gradient); 0: none needed
- * or none used.  Results do not depend on the workspace beyond the order of their
- * fp32 sums. */
+ * or none used.  With it the product is summed by the tensor cores, whose fp32
+ * additions truncate (the runs of an fp32 weight gradient aside, an error that grows
+ * with the length of the sum: 1.9e-5 relative at 16384 terms), without it by fused
+ * multiply-adds that round to nearest: the results differ by those roundings. */
 MUON_API size_t muon_expert_workspace_size(int kind, const void* a, long long ld_a, const void* b, long long ld_b,
                                            long long stride_b, int experts, long long rows, int inner, int outer,
                                            int dtype);

@@ -946,7 +946,9 @@ def muon_expert_product(xs: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor
     expert owns keep their contents.  bf16 and fp16 run on the tensor cores
     (operands whose bases and strides are no multiples of 16 bytes after a copy
     into rows that are; small ones of that kind on the CUDA cores), fp32 on the
-    CUDA cores.  ``status``: one int32 word for a device-side timeout.
+    CUDA cores.  ``status``: one int32 word, MUON_STATUS_TIMEOUT (2) where a
+    device-side wait gave up and rows stayed unwritten; without it nothing
+    reports that.
     """
     device, dtype, code, rows, width, ld = _lead(xs, "xs")
     experts = _offsets_arg(offsets, device)
