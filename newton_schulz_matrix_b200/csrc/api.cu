@@ -550,7 +550,7 @@ int run_chain(const Ctx& c, const Layout& L, const Bufs& B, int chunk, const muo
   return 0;
 }
 
-// Host-side slot table of the fused update (about 7 KB): one per host thread,
+// Host-side slot table of the fused update (about 9 KB): one per host thread,
 // reused for every chunk; its contents are copied into the kernel parameters
 // at launch, so reuse after the launch call is safe.
 UpdateSlots& slots_storage() {

@@ -35,18 +35,22 @@
 // warp waits, and once that warp of both CTAs has zeroed its rows and arrived,
 // the leader's "full" barrier opens.  The producers meanwhile go on to the next
 // tiles (waiting for that load in the producer itself emptied the ring at every
-// tile: 334 against 303 us at 49152 rows over 64 experts of 1408 x 2048).
+// tile and took a tenth longer).  49152 rows over 64 experts of 1408 x 2048, bf16:
+// forward 254, input gradient 244, weight gradient 291 us each after a rest, at the full
+// clock of 1965 MHz; 295, 281 and 330 us over seconds under the power cap, which
+// leaves 1.39 to 1.53 GHz (a dense library product of the forward's size there: 238).
 //
 // fp32 weight gradients.  The tensor cores truncate when they add to an fp32
-// accumulator, a bias that grows with the length of the sum (relative error
-// 1.3e-6 at 1024 tokens, 4.9e-6 at 4096, 1.9e-5 at 16384).  Where the result is
+// accumulator, a bias that grows with the length of the sum (relative error of one
+// sum 1.3e-6 at 1024 tokens, 4.9e-6 at 4096, 1.9e-5 at 16384).  Where the result is
 // stored in fp32 a tile is therefore summed in runs of 512 tokens, each in a
 // fresh accumulator (two in TMEM), and the epilogue warps add the runs in
 // registers with round-to-nearest, 128 sums a thread, while the next run's MMAs
-// go on: 6.5e-7 at every length (a plain fp32 product 5.6e-7 at 1024 tokens), at
-// 270 us where the 16-bit result takes 240 (8192 rows, 8 experts of
-// 2048 x 7168).  Sixteen epilogue warps of 64 sums leave room for five stages
-// only: 311 us.
+// go on: 6.5e-7 in fp16 and 4.8e-7 in bf16 at every length to 16384 (fp32 operands on
+// the CUDA cores 5.7e-7 at 1024 tokens, 2.3e-6 at 16384), at 277 us where the 16-bit
+// result takes 250 (8192 rows, 8 experts of 2048 x 7168, under the power cap).
+// Sixteen epilogue warps of 64 sums leave room for five stages only, and took 15 %
+// longer.
 //
 // Waits are bounded as in the other product kernels.
 #include <algorithm>

@@ -66,7 +66,7 @@ __device__ __forceinline__ void mma_pair(uint32_t d_tmem, uint64_t adesc, uint64
       : "memory");
 }
 // Kernel parameter of launches without the fused update (keeps their
-// parameter block small; UpdateSlots is ~7 KB).
+// parameter block small; UpdateSlots is ~9 KB).
 struct NoUpdate {
   int unused;
 };

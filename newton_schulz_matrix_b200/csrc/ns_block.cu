@@ -45,6 +45,13 @@
 // Blocks whose rows start anywhere load element by element, whole pieces at a time:
 // 64 of 127 x 2047 take 225 us (297 with one load after the other).
 //
+// Every block that fits takes this launch.  Steps by separate products and here, us
+// (bf16 W and G, dense blocks that each are a tensor): 64 of 128 x 2048 317 and 170,
+// one 165 and 76; 64 of 128 x 4096 (clusters of eight) 515 and 401, 16 264 and 150,
+// 64 of 64 x 4096 384 and 355; 256 of 128 x 512 302 and 121; few rows, padded to 128:
+// 512 of 8 x 256 267 and 122, 512 of 16 x 1024 634 and 407, 128 of 32 x 2048 331 and
+// 262, 64 of 64 x 640 140 and 60.
+//
 // Waits on mbarriers are bounded; on expiry a CTA raises its abort flag, skips
 // its further waits and still takes part in every cluster barrier, so that none
 // is left waiting, then reports through the error word.
