@@ -293,9 +293,9 @@ def _apart(t: torch.Tensor, name: str):
         span += (n - 1) * stride
     else:
         return
-    starts = torch.zeros(1, dtype=torch.int64)  # strides that interleave: the rows themselves
+    starts = torch.zeros(1, dtype=torch.int64, device="cpu")  # strides that interleave: the rows themselves
     for stride, n in lead:
-        starts = (starts[:, None] + stride * torch.arange(n)).view(-1)
+        starts = (starts[:, None] + stride * torch.arange(n, device="cpu")).view(-1)
     if bool((starts.sort().values.diff() < cols).any()):
         raise MuonError(f"{name} overlaps itself")
 

@@ -360,3 +360,11 @@ assert lib.muon_step_blocks(blocks, n, ctypes.byref(hp), ws, 1 << 30, None, None
 """.format(root=ROOT)
     run = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
     assert run.returncode == 0, (run.returncode, run.stderr[-500:])
+
+
+def test_overlap_is_found_on_the_host_whatever_the_default_device():
+    w, m = Fake((3, 2, 2), (4, 6, 1)), Fake((3, 2, 2), dtype=torch.float32)
+    with torch.device("meta"):
+        assert nsm._build_block_groups([w], [w], [m], [None])[1] == 1
+        with pytest.raises(nsm.MuonError, match="overlaps"):
+            nsm._build_block_groups([Fake((3, 2, 2), (4, 5, 1))], [w], [m], [None])
