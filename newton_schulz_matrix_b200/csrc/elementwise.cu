@@ -134,6 +134,18 @@ __device__ __forceinline__ float block_sum_fixed(float v, float* red) {
 // and 16 elements each, consecutive 16-byte accesses of a thread each touched
 // half of a sector: half the L1 requests were repeats, and the pack slowed with
 // the SM clock under the power cap.)
+//
+// U is one fused multiply-add of two products, and which of them is rounded first
+// shows in its last bit.  It goes by the matrix's own shape, (1 - mu) G exact in whole
+// tiles of rows of whole 8s and mu M elsewhere, whatever the pitch and alignment
+// that choose how the elements are accessed: a block gets the bits of its dense copy,
+// and a gradient the same ones in every type that holds it.
+__device__ __forceinline__ float momentum(float mu, float m, float g) { return __fmaf_rn(mu, m, __fmul_rn(1.f - mu, g)); }
+template <bool WHOLE>
+__device__ __forceinline__ float nesterov_u(float mu, float m, float g) {
+  return WHOLE ? __fmaf_rn(1.f - mu, g, __fmul_rn(mu, m)) : __fmaf_rn(mu, m, __fmul_rn(1.f - mu, g));
+}
+
 template <typename TS, typename TX, bool MOMENTUM, bool TRANS>
 __global__ void __launch_bounds__(kPackThreads)
 pack_kernel(const PackArgs a, const __grid_constant__ SegmentPtrs p) {
@@ -152,6 +164,21 @@ pack_kernel(const PackArgs a, const __grid_constant__ SegmentPtrs p) {
   const bool full = inside && a.vec;
   const bool store = a.pass != 1;
   float u[4][4];  // [row pass][element]
+  // M and U of four elements
+  auto advance = [&](const float (&g)[4], float (&m)[4], float (&out)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m[i] = momentum(a.mu, m[i], g[i]);
+    if (!a.nesterov) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) out[i] = m[i];
+    } else if (inside && a.cols % 8 == 0) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) out[i] = nesterov_u<true>(a.mu, m[i], g[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) out[i] = nesterov_u<false>(a.mu, m[i], g[i]);
+    }
+  };
   if (full) {
     // every load of the four passes first: one memory round trip per thread
     float g[4][4], m[4][4];
@@ -164,11 +191,7 @@ pack_kernel(const PackArgs a, const __grid_constant__ SegmentPtrs p) {
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       if (MOMENTUM) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          m[q][i] = a.mu * m[q][i] + (1.f - a.mu) * g[q][i];
-          u[q][i] = a.nesterov ? (1.f - a.mu) * g[q][i] + a.mu * m[q][i] : m[q][i];
-        }
+        advance(g[q], m[q], u[q]);
         if (store) store4(mom + (long long)(r0 + q * 16 + lr) * a.ld_mom + c0 + lc, m[q]);
       } else {
 #pragma unroll
@@ -177,7 +200,7 @@ pack_kernel(const PackArgs a, const __grid_constant__ SegmentPtrs p) {
     }
   } else {
     // the same elements per thread, and again every load before the first store
-    // (rows that start anywhere, and ragged tiles)
+    // (rows that start anywhere, and ragged tiles; zeros outside them give zeros)
     float g[4][4], m[4][4];
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
@@ -192,19 +215,15 @@ pack_kernel(const PackArgs a, const __grid_constant__ SegmentPtrs p) {
     }
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      const long long r = r0 + q * 16 + lr;
+      if (MOMENTUM) {
+        const long long r = r0 + q * 16 + lr;
+        advance(g[q], m[q], u[q]);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int c = c0 + lc + i;
-        if (!(r < a.rows && c < a.cols)) {
-          u[q][i] = 0.f;
-        } else if (MOMENTUM) {
-          const float mv = a.mu * m[q][i] + (1.f - a.mu) * g[q][i];
-          if (store) mom[r * a.ld_mom + c] = mv;
-          u[q][i] = a.nesterov ? (1.f - a.mu) * g[q][i] + a.mu * mv : mv;
-        } else {
-          u[q][i] = g[q][i];
-        }
+        for (int i = 0; i < 4; ++i)
+          if (store && r < a.rows && c0 + lc + i < a.cols) mom[r * a.ld_mom + c0 + lc + i] = m[q][i];
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) u[q][i] = g[q][i];
       }
     }
   }

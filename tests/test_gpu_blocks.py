@@ -331,3 +331,37 @@ def test_one_launch_does_not_shrink_with_the_workspace():
         launches.append({r["kernel"]: r["launches"] for r in nsm.muon_profile_end()}["ns_block_kernel"])
     assert launches == [2, 2]
     assert torch.equal(w, w2) and torch.equal(m, m2) and bool((store[lo:] == 7).all())
+
+
+@pytest.mark.parametrize("block", [(192, 256), (256, 192), (200, 328), (300, 140), (257, 259), (516, 388)])
+@pytest.mark.parametrize("gdt", ["bf16", "fp32"])
+def test_alignment_does_not_show_in_the_bits(block, gdt):
+    """A block is its dense copy bit for bit where the two are accessed differently: rows of whole 8s at odd
+    pitches and addresses, other rows at pitches of whole 8s."""
+    for i, (pad, first) in enumerate(((0, 0), (1, 1), (8, 0), (3, 2), (4, 4))):
+        pitch = 2 * block[1] + pad
+        for hp in ({}, {"compute_dtype": "fp32"}, {"compute_dtype": "bf16", "mode": "gram_stabilized"}, {"nesterov": False}):
+            stores = [torch.full((2, block[0], -(-pitch // 8) * 8 + 8 if pad == 8 else pitch + first), 7.0, dtype=dt, device="cuda")
+                      for dt in (torch.float32, TYPES[gdt], torch.float32)]
+            w, g, m = (s[:, :, first:first + 2 * block[1]] for s in stores)
+            for k, (t, std) in enumerate(((w, 0.05), (g, 1.0), (m, 0.2))):
+                t.copy_(synth.gaussian(1, t.numel(), 230 + 3 * i + k, "cuda", std=std).view(t.shape))
+            wd, gd, md = (cut(t, block) for t in (w, g, m))
+            nsm.muon_step(wd, gd, md, **hp)
+            nsm.muon_step_blocks([w], [g], [m], [block], **hp)
+            for got, want in zip(cut(w, block) + cut(m, block), wd + md):
+                assert torch.equal(got, want), (pad, first, hp)
+
+
+@pytest.mark.parametrize("shape", [(384, 388), (100, 100), (516, 516), (300, 700), (256, 512), (257, 259)])
+@pytest.mark.parametrize("hp", [{}, {"compute_dtype": "fp32"}, {"mode": "gram_stabilized"}], ids=["fp16", "fp32", "gram"])
+def test_a_gradient_steps_alike_in_every_type_that_holds_it(shape, hp):
+    """muon_step on the same values of G in bf16 and fp32, whose rows are aligned differently."""
+    results = []
+    for dt in (torch.bfloat16, torch.float32):
+        w, m = (synth.gaussian(*shape, 250 + k, "cuda", std=std) for k, std in enumerate((0.05, 0.2)))
+        g = synth.gaussian(*shape, 252, "cuda").bfloat16().to(dt)
+        nsm.muon_step([w], [g], [m], **hp)
+        results.append((w, m))
+    for a, b in zip(*results):
+        assert torch.equal(a, b)
