@@ -27,6 +27,10 @@
 // memory by ldmatrix.trans / stmatrix and stored by TMA, or row by row where
 // the expert's tokens end inside the box.
 //
+// A TMA store clips in whole 16 bytes: the last box of a row whose width is no
+// multiple of that would write up to 7 elements behind the row, into whatever a
+// result with a larger pitch has there.  Such boxes are stored element by element.
+//
 // The weight gradient's contraction runs over the segment's tokens, so its last
 // k-block may end inside the next expert's rows.  MMAs cover whole groups of 16
 // tokens; the rows of the last group beyond the segment are zeroed in shared
@@ -492,7 +496,7 @@ expert_kernel(const __grid_constant__ EMaps maps, const __grid_constant__ EParam
         for (int k = 0; k < 4; ++k)
           *reinterpret_cast<float4*>(S + sw64(lane, k)) =
               make_float4(sum[h * 16 + k * 4], sum[h * 16 + k * 4 + 1], sum[h * 16 + k * 4 + 2], sum[h * 16 + k * 4 + 3]);
-        if (!p.d_vec) {
+        if (!p.d_vec || ((p.C & 3) && gj + h * 16 + 16 > p.C)) {
           __syncwarp();
           const int col = gj + h * 16 + (lane & 15);
           float* d = reinterpret_cast<float*>(p.D) + tl.e * p.stride_d + col;
@@ -563,7 +567,7 @@ expert_kernel(const __grid_constant__ EMaps maps, const __grid_constant__ EParam
         __syncwarp();
 #pragma unroll
         for (int k = 0; k < 4; ++k) *reinterpret_cast<uint4*>(S + sw64(lane, k)) = dq[k];
-        if (WG && !p.d_vec) {
+        if (WG && (!p.d_vec || ((p.C & 7) && tl.c * 256 + c * 32 + 32 > p.C))) {
           __syncwarp();
           const int col = tl.c * 256 + c * 32 + lane;
           uint16_t* d = reinterpret_cast<uint16_t*>(p.D) + tl.e * p.stride_d + col;
@@ -601,11 +605,11 @@ expert_kernel(const __grid_constant__ EMaps maps, const __grid_constant__ EParam
             for (int k = 0; k < min(32, valid); ++k)
               if (fi + lane < p.F)
                 d[(row + k) * p.ldd] = *reinterpret_cast<const uint16_t*>(S + sw64(k, lane >> 3) + (lane & 7) * 2);
-          } else if (valid >= 32) {
+          } else if (valid >= 32 && (!(p.F & 7) || fi + 32 <= p.F)) {
             fence_async_smem();
             __syncwarp();
             if (lane == 0) {
-              tma_store_3d(&maps.d, s0, fi, row, 0);    // clips the features past F
+              tma_store_3d(&maps.d, s0, fi, row, 0);    // clips the features past F (whole 8s)
               bulk_commit();
             }
           } else {

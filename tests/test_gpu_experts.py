@@ -657,3 +657,40 @@ def test_expert_step_reports_its_weight_gradients():
         step.words[1].fill_(2)
         run()
         assert step.status.tolist() == [0] * 6
+
+
+@pytest.mark.parametrize("dtype", [BF, HF, SF])
+@pytest.mark.parametrize("counts,inner,outer", [([45, 44, 151, 66, 72, 0, 86], 7, 24), ([499], 325, 163), ([64, 33, 200], 171, 331),
+                                                ([5, 6, 11, 0, 32], 15, 560), ([1, 40], 1, 3), ([300, 41], 518, 263)])
+def test_results_of_ragged_rows_keep_what_lies_behind_them(counts, inner, outer, dtype):
+    """Results whose rows start on 16 bytes and end inside 16: the columns behind them stay, and the operands'
+    columns behind the rows (NaN) are not read."""
+    def wide(*shape, fill=7.0, dt=dtype):
+        store = torch.full((*shape[:-1], -(-shape[-1] // 8) * 8 + 8), fill, dtype=dt, device="cuda")
+        return store[..., :shape[-1]], store[..., shape[-1]:]
+
+    g = gen(44)
+    rows, nan = sum(counts) + 2, float("nan")
+    offsets = offsets_of(counts)
+    (xs, _), (dys, _), (w, _) = (wide(*s, fill=nan) for s in ((rows, inner), (rows, outer), (len(counts), outer, inner)))
+    for t in (xs, dys, w):
+        t.copy_(randn(g, *t.shape, dtype=dtype))
+    u = U_NEAREST if dtype == SF else U_TRUNCATED
+    (y, behind_y), (dx, behind_dx) = wide(rows, outer), wide(rows, inner)
+    nsm.muon_expert_product(xs, w, offsets, out=y)
+    nsm.muon_expert_input_grad(dys, w, offsets, out=dx)
+    results = []
+    for dt, accumulate in ((dtype, False), (SF, False), (SF, True)):
+        dw, behind = wide(len(counts), outer, inner, dt=dt)
+        dw.zero_()
+        nsm.muon_expert_weight_grad(dys, xs, offsets, out=dw, accumulate=accumulate)
+        assert bool((behind == 7).all()), (dt, accumulate)
+        results.append(dw)
+    assert bool((behind_y == 7).all()) and bool((behind_dx == 7).all())
+    assert bool((y[sum(counts):] == 7).all()) and bool((dx[sum(counts):] == 7).all())
+    for e, (lo, hi) in enumerate(segments(offsets, rows)):
+        x, d, m = f64(xs[lo:hi]), f64(dys[lo:hi]), f64(w[e])
+        close(y[lo:hi], x @ m.T, inner, x.abs() @ m.abs().T, u)
+        close(dx[lo:hi], d @ m, outer, d.abs() @ m.abs(), u)
+        for dw in results:
+            close(dw[e], d.T @ x, hi - lo, d.abs().T @ x.abs(), u)
