@@ -694,3 +694,42 @@ def test_results_of_ragged_rows_keep_what_lies_behind_them(counts, inner, outer,
         close(dx[lo:hi], d @ m, outer, d.abs() @ m.abs(), u)
         for dw in results:
             close(dw[e], d.T @ x, hi - lo, d.abs().T @ x.abs(), u)
+
+
+def test_calls_at_once_from_several_threads():
+    """Four threads, each on a stream of its own, run the operators and the block step at the same time, and get
+    what one after the other gives."""
+    import threading
+
+    def work(seed, stream=None):
+        g = gen(seed)
+        counts = [300, 0, 41, 170]
+        offsets, xs, dys, w = product_case(seed, counts, 256 + 8 * seed, 192, BF, tail=0)
+        ids, m = routing(seed, 3000, 4, 64, 0.1), randn(g, 8, 64, 512) * 0.1
+        p, gr = randn(g, 8, 64, 512, dtype=BF), randn(g, 8, 64, 512, dtype=BF)
+        wm = torch.zeros(*w.shape, device="cuda")
+        torch.cuda.current_stream().synchronize()
+        out = []
+        for _ in range(20):
+            offs, slot, source = nsm.muon_expert_sort(ids, 64, stream=stream)
+            y = nsm.muon_expert_product(xs, w, offsets, stream=stream)
+            dw = nsm.muon_expert_weight_grad(dys, xs, offsets, out_dtype=SF, stream=stream)
+            nsm.muon_step_blocks([p, w], [gr, dw], [m, wm], [(64, 256), None], stream=stream)
+            out = [offs, slot, source, y, dw, p, m, w, wm]
+        (stream or torch.cuda.current_stream()).synchronize()
+        return out
+
+    want = [work(60 + i) for i in range(4)]
+    got, streams = [None] * 4, [torch.cuda.Stream() for _ in range(4)]
+
+    def run(i):
+        with torch.cuda.stream(streams[i]):
+            got[i] = work(60 + i, streams[i])
+
+    threads = [threading.Thread(target=run, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    for a, b in zip(want, got):
+        assert all(torch.equal(x, y) for x, y in zip(a, b))
